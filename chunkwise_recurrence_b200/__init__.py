@@ -1,7 +1,8 @@
 """chunkwise_recurrence_b200 -- Python binding of libgdr.
 
 libgdr computes the chunkwise-parallel forward pass of the gated delta rule
-(DeltaNet, Gated DeltaNet and KDA) on one B200.  This module only marshals
+(DeltaNet, Gated DeltaNet and KDA) on one B200, and beside it a gated linear
+recurrence and layer normalisation.  This module only marshals
 arguments into the C ABI declared in ``include/gdr.h``; every step of the
 computation runs in the library's CUDA kernels.  PyTorch supplies device
 memory and streams.  There is no CPU fallback: if ``libgdr.so`` is missing the
@@ -9,6 +10,7 @@ calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -18,7 +20,8 @@ __all__ = ["chunk_fwd", "chunk_fwd_host", "chunk_fwd_noalloc",
            "chunk_fwd_segmented", "chunk_fwd_gdn2", "chunk_fwd_fg2",
            "decode_step", "decode_step_gdn2", "decode_step_fg2",
            "efla_beta", "efla_beta_backward", "backward", "backward_gdn2",
-           "backward_fg2",
+           "backward_fg2", "linear_fwd", "linear_step", "linear_backward",
+           "layer_norm", "layer_norm_backward",
            "device_error", "status_string",
            "algo_applies", "fused_tc_available",
            "GdrError", "load_library", "LIB_PATH", "GATES", "ALGOS",
@@ -40,9 +43,14 @@ EXPORTED_SYMBOLS = ("gdr_chunk_fwd", "gdr_chunk_fwd_host", "gdr_device_error",
                     "gdr_chunk_fwd_segmented", "gdr_chunk_fwd_gdn2",
                     "gdr_decode_step_gdn2", "gdr_chunk_fwd_fg2",
                     "gdr_decode_step_fg2", "gdr_backward_gdn2",
-                    "gdr_backward_fg2", "gdr_efla_beta_backward")
+                    "gdr_backward_fg2", "gdr_efla_beta_backward",
+                    "gdr_linear_fwd", "gdr_linear_step",
+                    "gdr_linear_backward", "gdr_layer_norm",
+                    "gdr_layer_norm_backward")
 # size of the static scratch array behind gdr_chunk_fwd_noalloc
 NOALLOC_SCRATCH_BYTES = 64 << 20
+# tokens between the states that linear_fwd keeps for linear_backward
+LINEAR_CHUNK = 32
 
 _lib = None
 
@@ -106,6 +114,21 @@ def load_library(path: str = LIB_PATH):
     lib.gdr_efla_beta.argtypes = [vp, fp, fp, i, i, i, i, vp]
     lib.gdr_efla_beta_backward.restype = ctypes.c_int
     lib.gdr_efla_beta_backward.argtypes = [vp, fp, fp, fp, fp, i, i, i, i, vp]
+    ll, f32 = ctypes.c_longlong, ctypes.c_float
+    lib.gdr_linear_fwd.restype = ctypes.c_int
+    lib.gdr_linear_fwd.argtypes = [vp, ll, fp, fp, vp, fp, fp, i, i, i, i, vp,
+                                   ctypes.POINTER(_Opts)]
+    lib.gdr_linear_step.restype = ctypes.c_int
+    lib.gdr_linear_step.argtypes = [vp, ll, fp, fp, fp, vp, i, i, i, vp,
+                                    ctypes.POINTER(_Opts)]
+    lib.gdr_linear_backward.restype = ctypes.c_int
+    lib.gdr_linear_backward.argtypes = [vp, ll, fp, fp, fp, vp, fp, vp, fp, fp,
+                                        i, i, i, i, vp, ctypes.POINTER(_Opts)]
+    lib.gdr_layer_norm.restype = ctypes.c_int
+    lib.gdr_layer_norm.argtypes = [vp, ll, fp, fp, vp, i, i, i, f32, i, vp]
+    lib.gdr_layer_norm_backward.restype = ctypes.c_int
+    lib.gdr_layer_norm_backward.argtypes = [vp, ll, fp, vp, vp, fp, fp, i, i,
+                                            i, f32, i, vp]
     lib.gdr_device_error.restype = ctypes.c_int
     lib.gdr_device_error.argtypes = [vp, i]
     lib.gdr_algo_applies.restype = ctypes.c_int
@@ -567,6 +590,282 @@ def efla_beta_backward(k, beta, d_beta_prime, dk, *, d_beta=None,
     if rc != 0:
         raise GdrError(rc, "gdr_efla_beta_backward")
     return d_beta
+
+
+# ---------------------------------------------------------------------------
+# Linear recurrence and layer normalisation.  Unlike the entries above, these
+# check every tensor (ValueError) before they call the library.
+
+def _activation(name, x, inner):
+    """Checks a device tensor of activations [.., inner dims] whose inner
+    dimensions are contiguous and whose tokens are evenly spaced; returns the
+    distance between tokens in elements."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype not in DTYPES:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    step = 1
+    shape, strides = x.shape, x.stride()
+    for i in range(x.dim() - 1, x.dim() - 1 - inner, -1):
+        if shape[i] != 1 and strides[i] != step:
+            raise ValueError(f"{name}: the last {inner} dimension(s) must be "
+                             "contiguous")
+        step *= shape[i]
+    ld, rows = None, 1
+    if x.numel():
+        for i in range(x.dim() - 1 - inner, -1, -1):
+            if shape[i] == 1:
+                continue
+            if ld is None:
+                ld = strides[i]
+                if ld < step:
+                    raise ValueError(f"{name}: tokens must not overlap")
+            elif strides[i] != ld * rows:
+                raise ValueError(f"{name}: tokens must be evenly spaced")
+            rows *= shape[i]
+    return step if ld is None else ld
+
+
+def _check(name, t, shape, dtype, x):
+    if t is None:
+        return
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, "
+                         f"not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != x.device:
+        raise ValueError(f"{name} must be on {x.device}, not {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on_stream(x, stream):
+    """(stream, a context to allocate and launch in): new tensors then belong
+    to that stream and the current device is x's."""
+    current = torch.cuda.current_stream(x.device)
+    if stream is None or stream == current:
+        if x.device.index == torch.cuda.current_device():
+            return current, contextlib.nullcontext()
+        return current, torch.cuda.device(x.device)
+    if stream.device != x.device:
+        raise ValueError(f"the stream must be on {x.device}")
+    return stream, torch.cuda.stream(stream)
+
+
+def _linear_args(x, log_alpha, initial_state, gate, cu_seqlens):
+    if x.dim() != 4:
+        raise ValueError("x must be [B, T, H, d]")
+    ldx = _activation("x", x, 2)
+    B, T, H, d = x.shape
+    nseq = B
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("packed sequences (cu_seqlens) need B = 1")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [num_seqs + 1]")
+        _check("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, x)
+        nseq = cu_seqlens.numel() - 1
+    g = _linear_gate(x, log_alpha, gate)
+    _check("initial_state", initial_state, (nseq, H, d), torch.float32, x)
+    opts = _Opts(DTYPES[x.dtype], GATES[g],
+                 None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                 nseq if cu_seqlens is not None else 0, ALGOS["auto"])
+    return ldx, B, T, H, d, nseq, opts
+
+
+def _linear_gate(x, log_alpha, gate):
+    if gate is None:
+        gate = ("none" if log_alpha is None else
+                "scalar" if log_alpha.dim() == x.dim() - 1 else "channel")
+    if gate not in GATES:
+        raise ValueError(f"gate must be one of {sorted(GATES)}")
+    if (gate == "none") != (log_alpha is None):
+        raise ValueError("log_alpha must be given for a gate, and only then")
+    _check("log_alpha", log_alpha,
+           x.shape[:-1] if gate == "scalar" else x.shape, torch.float32, x)
+    return gate
+
+
+def linear_fwd(x, log_alpha=None, initial_state=None, *,
+               gate: str | None = None, cu_seqlens=None, out=None,
+               final_state=None, output_final_state: bool = True,
+               output_chunk_states: bool = False, stream=None):
+    """Run ``gdr_linear_fwd``: the gated linear recurrence
+    h_t = e^log_alpha_t h_{t-1} + x_t, out_t = h_t.
+
+    x [B, T, H, d] (bf16 or fp32; tokens may be evenly spaced columns of a
+    wider tensor); log_alpha [B, T, H] (scalar gate), [B, T, H, d] (channel
+    gate) or None, fp32; initial_state [N, H, d] fp32 or None (zero), N = B or
+    the number of packed sequences.  Returns (out, final_state), or (out,
+    final_state, chunk_states) with ``output_chunk_states``: pass the latter
+    to ``linear_backward``.  final_state is None if not requested.
+    """
+    lib = load_library()
+    ldx, B, T, H, d, nseq, opts = _linear_args(x, log_alpha, initial_state,
+                                               gate, cu_seqlens)
+    _check("out", out, x.shape, x.dtype, x)
+    _check("final_state", final_state, (nseq, H, d), torch.float32, x)
+    stream, on = _on_stream(x, stream)
+    with on:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if final_state is None and output_final_state:
+            final_state = torch.empty(nseq, H, d, dtype=torch.float32,
+                                      device=x.device)
+        chunk_states = None
+        if output_chunk_states:
+            chunk_states = torch.empty(B * T // LINEAR_CHUNK + nseq, H, d,
+                                       dtype=torch.float32, device=x.device)
+        rc = lib.gdr_linear_fwd(_ptr(x), ldx, _ptr(log_alpha),
+                                _ptr(initial_state), _ptr(out),
+                                _ptr(final_state), _ptr(chunk_states), B, T,
+                                H, d, ctypes.c_void_p(stream.cuda_stream),
+                                ctypes.byref(opts))
+    if rc != 0:
+        raise GdrError(rc, "gdr_linear_fwd")
+    if output_chunk_states:
+        return out, final_state, chunk_states
+    return out, final_state
+
+
+def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
+                gate: str | None = None, stream=None):
+    """Run ``gdr_linear_step``: one token per sequence of the gated linear
+    recurrence.
+
+    x [N, H, d]; log_alpha [N, H] (scalar gate), [N, H, d] (channel gate) or
+    None; state [N, H, d] fp32 or None (zero).  ``state_out`` defaults to
+    ``state`` itself (an in-place update) when a state is given, else a new
+    tensor.  Returns (out [N, H, d], state_out).
+    """
+    lib = load_library()
+    if x.dim() != 3:
+        raise ValueError("x must be [N, H, d]")
+    ldx = _activation("x", x, 2)
+    N, H, d = x.shape
+    g = _linear_gate(x, log_alpha, gate)
+    _check("state", state, x.shape, torch.float32, x)
+    _check("out", out, x.shape, x.dtype, x)
+    _check("state_out", state_out, x.shape, torch.float32, x)
+    opts = _Opts(DTYPES[x.dtype], GATES[g], None, 0, ALGOS["auto"])
+    stream, on = _on_stream(x, stream)
+    with on:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if state_out is None:
+            state_out = state if state is not None else torch.empty(
+                N, H, d, dtype=torch.float32, device=x.device)
+        rc = lib.gdr_linear_step(_ptr(x), ldx, _ptr(log_alpha), _ptr(state),
+                                 _ptr(state_out), _ptr(out), N, H, d,
+                                 ctypes.c_void_p(stream.cuda_stream),
+                                 ctypes.byref(opts))
+    if rc != 0:
+        raise GdrError(rc, "gdr_linear_step")
+    return out, state_out
+
+
+def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
+                    chunk_states=None, gate: str | None = None,
+                    cu_seqlens=None, need_initial_state_grad: bool = True,
+                    stream=None):
+    """Run ``gdr_linear_backward``: gradients of ``linear_fwd``'s outputs
+    (same inputs) given dL/d out (the shape and dtype of x, contiguous) and,
+    optionally, dL/d final_state.  ``chunk_states`` as ``linear_fwd`` returned
+    it for these inputs, or None (computed again).  Returns a dict of CUDA
+    tensors dx (the dtype of x), dlog_alpha (fp32; None without a gate) and
+    dinitial_state (fp32; None unless requested)."""
+    lib = load_library()
+    ldx, B, T, H, d, nseq, opts = _linear_args(x, log_alpha, initial_state,
+                                               gate, cu_seqlens)
+    _check("d_out", d_out, x.shape, x.dtype, x)
+    _check("d_final_state", d_final_state, (nseq, H, d), torch.float32, x)
+    _check("chunk_states", chunk_states,
+           (B * T // LINEAR_CHUNK + nseq, H, d), torch.float32, x)
+    stream, on = _on_stream(x, stream)
+    with on:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        gla = None if log_alpha is None else torch.empty(
+            log_alpha.shape, dtype=torch.float32, device=x.device)
+        gs0 = (torch.empty(nseq, H, d, dtype=torch.float32, device=x.device)
+               if need_initial_state_grad else None)
+        rc = lib.gdr_linear_backward(
+            _ptr(x), ldx, _ptr(log_alpha), _ptr(initial_state),
+            _ptr(chunk_states), _ptr(d_out), _ptr(d_final_state), _ptr(dx),
+            _ptr(gla), _ptr(gs0), B, T, H, d,
+            ctypes.c_void_p(stream.cuda_stream), ctypes.byref(opts))
+    if rc != 0:
+        raise GdrError(rc, "gdr_linear_backward")
+    return dict(dx=dx, dlog_alpha=gla, dinitial_state=gs0)
+
+
+def _norm_args(x, weight):
+    """(ldx, number of tokens, heads, channels, the parameters' shape)."""
+    if weight is not None and weight.dim() not in (1, 2):
+        raise ValueError("weight must be [d] or [H, d]")
+    inner = 1 if weight is None else weight.dim()
+    if x.dim() < inner:
+        raise ValueError("x must be [.., d], or [.., H, d] with a weight "
+                         "[H, d]")
+    ldx = _activation("x", x, inner)
+    shape = x.shape[x.dim() - inner:]
+    _check("weight", weight, shape, torch.float32, x)
+    H, d = (1, shape[0]) if inner == 1 else shape
+    ntok = 1
+    for n in x.shape[:x.dim() - inner]:
+        ntok *= n
+    return ldx, ntok, H, d, shape
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
+               stream=None):
+    """Run ``gdr_layer_norm``: (x - mean) / sqrt(var + eps) * weight + bias
+    over the last dimension.  x [.., d] with weight and bias [d] (fp32 or
+    None), or x [.., H, d] with parameters [H, d], one row of them per head.
+    A bias needs a weight.  Tokens of x may be evenly spaced columns of a
+    wider tensor."""
+    lib = load_library()
+    if bias is not None and weight is None:
+        raise ValueError("a bias needs a weight")
+    ldx, ntok, H, d, shape = _norm_args(x, weight)
+    _check("bias", bias, shape, torch.float32, x)
+    _check("out", out, x.shape, x.dtype, x)
+    stream, on = _on_stream(x, stream)
+    with on:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        rc = lib.gdr_layer_norm(_ptr(x), ldx, _ptr(weight), _ptr(bias),
+                                _ptr(out), ntok, H, d, eps, DTYPES[x.dtype],
+                                ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise GdrError(rc, "gdr_layer_norm")
+    return out
+
+
+def layer_norm_backward(x, weight, d_out, *, eps: float = 1e-5,
+                        need_param_grads: bool = True, stream=None):
+    """Run ``gdr_layer_norm_backward``: gradients of ``layer_norm`` (same x,
+    weight and eps) given dL/d out (the shape and dtype of x, contiguous).
+    Returns a dict of CUDA tensors dx (the dtype of x), dweight and dbias
+    (fp32, the shape of weight; None without a weight or if not needed)."""
+    lib = load_library()
+    ldx, ntok, H, d, shape = _norm_args(x, weight)
+    _check("d_out", d_out, x.shape, x.dtype, x)
+    params = need_param_grads and weight is not None
+    stream, on = _on_stream(x, stream)
+    with on:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw = db = None
+        if params:
+            dw = torch.empty(shape, dtype=torch.float32, device=x.device)
+            db = torch.empty(shape, dtype=torch.float32, device=x.device)
+        rc = lib.gdr_layer_norm_backward(
+            _ptr(x), ldx, _ptr(weight), _ptr(d_out), _ptr(dx), _ptr(dw),
+            _ptr(db), ntok, H, d, eps, DTYPES[x.dtype],
+            ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise GdrError(rc, "gdr_layer_norm_backward")
+    return dict(dx=dx, dweight=dw, dbias=db)
 
 
 def device_error(stream=None, clear: bool = True) -> int:

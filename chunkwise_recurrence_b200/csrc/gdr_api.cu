@@ -244,6 +244,14 @@ constexpr int kMaxHostDevices = 64;
 std::mutex g_host_mu;
 HostCtx g_host_ctx[kMaxHostDevices];
 
+// Lets this thread create resources that no capture records, whatever
+// capture mode is in force.
+struct RelaxedCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 gdr_status host_ctx(HostCtx *out) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return GDR_ERR_CUDA;
@@ -257,6 +265,8 @@ gdr_status host_ctx(HostCtx *out) {
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
     cudaMemPool_t pool = nullptr;
+    // (the first call may come while its stream is being captured)
+    RelaxedCapture relaxed;
     if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) return GDR_ERR_CUDA;
     uint64_t keep = UINT64_MAX;
     cudaStream_t up = nullptr, down = nullptr;
@@ -438,6 +448,28 @@ gdr_status host_by_time(const Problem &p, const gdr_opts &o, const void *q,
 }
 
 }  // namespace
+
+namespace gdr {
+
+gdr_status scratch_get(void **ptr, size_t bytes, cudaStream_t s) {
+  *ptr = nullptr;
+  if (alloc_fault_injected()) return GDR_ERR_OUT_OF_MEMORY;
+  HostCtx hc;
+  const gdr_status st = host_ctx(&hc);
+  if (st != GDR_OK) return st;
+  const cudaError_t e = cudaMallocFromPoolAsync(ptr, bytes, hc.pool, s);
+  if (e == cudaErrorMemoryAllocation) {
+    (void)cudaGetLastError();
+    return GDR_ERR_OUT_OF_MEMORY;
+  }
+  return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+}
+
+cudaError_t scratch_put(void *ptr, cudaStream_t s) {
+  return cudaFreeAsync(ptr, s);
+}
+
+}  // namespace gdr
 
 extern "C" gdr_status gdr_chunk_fwd_host(const void *q, const void *k,
                                          const void *v, const float *log_alpha,

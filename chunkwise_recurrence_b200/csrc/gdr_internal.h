@@ -46,6 +46,11 @@ struct Problem {
   const float *wkey = nullptr;
 };
 
+// Scratch of `bytes` bytes, stream-ordered on `s`, from the library's
+// per-device pool (csrc/gdr_api.cu), which keeps its memory between calls.
+gdr_status scratch_get(void **ptr, size_t bytes, cudaStream_t s);
+cudaError_t scratch_put(void *ptr, cudaStream_t s);
+
 // Staged path: four kernels + a chunk-table kernel, fp32 CUDA-core math.
 size_t staged_workspace_bytes(const Problem &p);
 cudaError_t staged_run(const Problem &p, void *workspace, cudaStream_t s);

@@ -591,6 +591,129 @@ GDR_API gdr_status gdr_efla_beta_backward(const void *k, const float *beta,
                                           cudaStream_t stream);
 
 /*
+ * gdr_linear_fwd -- gated linear recurrence with a vector state.
+ *
+ * The gated memory without the delta rule's erase and without keys: per
+ * sequence, head and channel
+ *     h_t = alpha_t h_{t-1} + x_t,   out_t = h_t,   alpha = e^{log_alpha}
+ * with opts->gate NONE (alpha = 1, a prefix sum), SCALAR (one decay per token
+ * and head) or CHANNEL (one per token and channel).
+ *
+ * Device pointers, 16-byte aligned, row-major:
+ *   x             [B][T][H][d]  dtype, tokens ldx >= H d elements apart (a
+ *                 column range of a wider projection); ldx = H d: contiguous
+ *   log_alpha     NULL (NONE), [B][T][H] (SCALAR) or [B][T][H][d] (CHANNEL)
+ *                 fp32, expected <= 0; -inf clears the state
+ *   initial_state [N][H][d] fp32, or NULL for a zero state
+ *   out           [B][T][H][d]  dtype (written)
+ *   final_state   [N][H][d] fp32 (written), or NULL to skip; a sequence of no
+ *                 tokens ends in its initial state
+ *   chunk_states  [T_all / GDR_LINEAR_CHUNK + N][H][d] fp32 (written), or
+ *                 NULL to skip: the state in front of every 32nd token of
+ *                 every sequence, for gdr_linear_backward, which else has to
+ *                 compute them again.  T_all is B * T, or T with cu_seqlens;
+ *                 sequence n, whose first token is a, has the entries from
+ *                 a / 32 + n on; entries between are not written.
+ * where N = B, or num_seqs with cu_seqlens (then B = 1).  Offsets have to be
+ * non-decreasing within [0, T]; rows of out outside every sequence are left
+ * as they were.  Buffers that are written must not overlap any other.
+ *
+ * Sizes: B, T, H >= 0, d >= 1, H <= 65535, H d <= 2^24; at most 2^28
+ * (sequence, 32-channel) pairs.  State and sums are fp32; out is rounded
+ * once.  opts->algo must be AUTO.  One launch, no scratch; results do not
+ * depend on scheduling.
+ */
+#define GDR_LINEAR_CHUNK 32
+
+GDR_API gdr_status gdr_linear_fwd(const void *x, long long ldx,
+                                  const float *log_alpha,
+                                  const float *initial_state, void *out,
+                                  float *final_state, float *chunk_states,
+                                  int B, int T, int H, int d,
+                                  cudaStream_t stream, const gdr_opts *opts);
+
+/*
+ * gdr_linear_step -- gdr_linear_fwd for one token per sequence, as used when
+ * generating one token at a time:  h' = alpha h + x,  out = h'.
+ *
+ * x [N][H][d] dtype, rows ldx apart; log_alpha NULL, [N][H] or [N][H][d];
+ * state_in [N][H][d] fp32 or NULL (zero); state_out [N][H][d] fp32 (written),
+ * which may be state_in itself; out [N][H][d] dtype (written).  No
+ * cu_seqlens.  Limits and status codes as for gdr_linear_fwd.
+ */
+GDR_API gdr_status gdr_linear_step(const void *x, long long ldx,
+                                   const float *log_alpha,
+                                   const float *state_in, float *state_out,
+                                   void *out, int N, int H, int d,
+                                   cudaStream_t stream, const gdr_opts *opts);
+
+/*
+ * gdr_linear_backward -- gradients of gdr_linear_fwd:
+ *     G_t = d_out_t + alpha_{t+1} G_{t+1}  (+ d_final_state at the last t)
+ *     dx_t = G_t,   d_log_alpha_t = G_t alpha_t h_{t-1}
+ *     d_initial_state = alpha_1 G_1
+ * h is computed again in fp32 from x, log_alpha and the chunk states; the
+ * rounded out is not needed.
+ *
+ * x, ldx, log_alpha, initial_state, sizes and opts as for gdr_linear_fwd;
+ * chunk_states as gdr_linear_fwd wrote it for the same inputs, or NULL.
+ *   d_out           [B][T][H][d] dtype;
+ *   d_final_state   [N][H][d] fp32, or NULL for zero;
+ *   dx              [B][T][H][d] dtype (written), so that it can be the d_out
+ *                   of what came before;
+ *   d_log_alpha     fp32, the layout of log_alpha (written; for SCALAR summed
+ *                   over the head's channels in a fixed order); NULL iff the
+ *                   gate is NONE;
+ *   d_initial_state [N][H][d] fp32 (written), or NULL to skip.
+ * Rows outside every sequence are left as they were.  Scratch, only where
+ * needed: the chunk states if they are not given (a forward pass more), and
+ * for SCALAR with d > 32 (d + 31) / 32 copies of d_log_alpha; stream-ordered
+ * from the library's pool, GDR_ERR_OUT_OF_MEMORY on failure.
+ */
+GDR_API gdr_status gdr_linear_backward(
+    const void *x, long long ldx, const float *log_alpha,
+    const float *initial_state, const float *chunk_states, const void *d_out,
+    const float *d_final_state, void *dx, float *d_log_alpha,
+    float *d_initial_state, int B, int T, int H, int d, cudaStream_t stream,
+    const gdr_opts *opts);
+
+/*
+ * gdr_layer_norm -- layer normalisation of every (token, head) row:
+ *     y = (x - mean) / sqrt(var + eps) w + b
+ * over the row's d channels (var: the mean squared distance from the mean).
+ * H = 1 with d the model's width in front of a token mixer; H heads of d
+ * channels, with their own parameters, behind it.
+ *
+ * Device pointers, 16-byte aligned: x [ntok][H][d] in `dtype`, tokens
+ * ldx >= H d elements apart; weight and bias [H][d] fp32, or NULL (ones,
+ * zeros); out [ntok][H][d] in `dtype` (written; must not overlap the rest).
+ * 1 <= d <= 16384, H <= 65535, ntok H < 2^31, eps >= 0.  ntok H == 0 is a
+ * no-op.  Statistics in fp32, the variance from distances to the mean; y is
+ * rounded once.  One launch, no scratch.
+ */
+GDR_API gdr_status gdr_layer_norm(const void *x, long long ldx,
+                                  const float *weight, const float *bias,
+                                  void *out, int ntok, int H, int d,
+                                  float eps, gdr_dtype dtype,
+                                  cudaStream_t stream);
+
+/*
+ * gdr_layer_norm_backward -- gradients of gdr_layer_norm, from x and d_out
+ * (the statistics are computed again from the row at hand).
+ *
+ * x, ldx, weight, sizes, eps and dtype as for gdr_layer_norm; d_out
+ * [ntok][H][d] in `dtype`; dx the same (written); d_weight and d_bias [H][d]
+ * fp32 (written, summed over the tokens in fp32 and in a fixed order), each
+ * NULL to skip.  With no token dx is empty and the sums are zero.  Scratch
+ * for d_weight and d_bias: up to 444 rows of H d floats each, stream-ordered
+ * from the library's pool; GDR_ERR_OUT_OF_MEMORY on failure.
+ */
+GDR_API gdr_status gdr_layer_norm_backward(
+    const void *x, long long ldx, const float *weight, const void *d_out,
+    void *dx, float *d_weight, float *d_bias, int ntok, int H, int d,
+    float eps, gdr_dtype dtype, cudaStream_t stream);
+
+/*
  * gdr_device_error -- synchronise `stream`, then read (and clear if `clear`)
  * the library's sticky device-side error word for the current device.
  * Returns GDR_OK if no kernel has reported an error, GDR_ERR_TIMEOUT if a

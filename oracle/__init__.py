@@ -20,6 +20,11 @@ Contents
                      token loop, small cases).
 ``gdn2_grads``       fp64 gradients of the Gated DeltaNet-2 loop (autograd), the
                      reference for a gate-aware backward pass.
+``linear_fwd``, ``linear_grads``
+                     the gated linear recurrence (a vector state, no erase) and
+                     its gradients (numpy token loops).
+``layer_norm``, ``layer_norm_grads``
+                     layer normalisation and its gradients.
 ``chunkwise_ref``    an independent fp64 chunkwise reformulation that solves the
                      intra-chunk triangular system with a dense ``solve``; it is a
                      pin for the token loop, not a second oracle for the GPU.
@@ -168,3 +173,5 @@ from .gdn2_ref import gdn2_fwd  # noqa: E402  (re-export)
 from .grad_ref import (efla_grads, fg2_grads, gdn2_grads,  # noqa: E402
                        gdr_grads)
 from .fg2_ref import fg2_fwd  # noqa: E402  (re-export)
+from .linear_ref import linear_fwd, linear_grads  # noqa: E402  (re-export)
+from .norm_ref import layer_norm, layer_norm_grads  # noqa: E402  (re-export)

@@ -1,0 +1,265 @@
+"""Linear recurrence and layer normalisation without a GPU: the fp64
+references are pinned by closed forms and central differences, and the C ABI
+rejects bad arguments on the host before any CUDA call."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import chunkwise_recurrence_b200 as gdr
+import oracle
+from chunkwise_recurrence_b200 import build as gdr_build
+
+OK, INVALID, UNSUPPORTED, CUDA, OOM = range(5)
+A = 0x10000       # 16-byte-aligned fake device addresses, far apart and never
+STEP = 1 << 40    # dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    gdr_build.build()
+    return gdr.load_library()
+
+
+def _rng(seed):
+    return np.random.default_rng(seed)
+
+
+# -------------------------------------------------------------- references
+
+def test_linear_prefix_sum_and_geometric_series():
+    x = _rng(0).normal(size=(2, 9, 2, 3))
+    out, fin, _ = oracle.linear_fwd(x)
+    assert np.allclose(out, np.cumsum(x, 1)) and np.allclose(fin, x.sum(1))
+    la = np.full((1, 40, 1), np.log(0.5))
+    out, _, _ = oracle.linear_fwd(np.ones((1, 40, 1, 2)), la)
+    t = np.arange(1, 41)
+    assert np.allclose(out[0, :, 0, 0], 2 * (1 - 0.5 ** t))
+
+
+def test_linear_split_and_packed_equal_one_call():
+    r = _rng(1)
+    x, la = r.normal(size=(1, 20, 2, 3)), -r.random((1, 20, 2, 3))
+    s0 = r.normal(size=(1, 2, 3))
+    out, fin, _ = oracle.linear_fwd(x, la, s0)
+    o1, f1, _ = oracle.linear_fwd(x[:, :7], la[:, :7], s0)
+    o2, f2, _ = oracle.linear_fwd(x[:, 7:], la[:, 7:], f1)
+    assert np.allclose(np.concatenate([o1, o2], 1), out)
+    assert np.allclose(f2, fin)
+    s = r.normal(size=(3, 2, 3))
+    cu = [0, 5, 5, 20]
+    po, pf, _ = oracle.linear_fwd(x, la, s, cu)
+    for n in range(3):
+        o, f, _ = oracle.linear_fwd(x[:, cu[n]:cu[n + 1]],
+                                    la[:, cu[n]:cu[n + 1]], s[n:n + 1])
+        assert np.allclose(po[:, cu[n]:cu[n + 1]], o)
+        assert np.allclose(pf[n:n + 1], f)
+
+
+@pytest.mark.parametrize("gate", ["none", "scalar", "channel"])
+def test_linear_gradients_are_the_differences(gate):
+    r = _rng(2)
+    cu = [0, 4, 4, 9]
+    x, s0 = r.normal(size=(1, 9, 2, 3)), r.normal(size=(3, 2, 3))
+    la = {"none": None, "scalar": -r.random((1, 9, 2)),
+          "channel": -r.random((1, 9, 2, 3))}[gate]
+    dO, dS = r.normal(size=x.shape), r.normal(size=s0.shape)
+
+    def loss(x, la, s0):
+        o, f, _ = oracle.linear_fwd(x, la, s0, cu)
+        return (o * dO).sum() + (f * dS).sum()
+
+    got = oracle.linear_grads(x, la, s0, dO, dS, cu)
+    for key, i in (("dx", 0), ("dlog_alpha", 1), ("dinitial_state", 2)):
+        args = [x, la, s0]
+        if args[i] is None:
+            assert got[key] is None
+            continue
+        num = np.zeros_like(args[i])
+        for j in np.ndindex(args[i].shape):
+            for sg in (1, -1):
+                a = args[i].copy()
+                a[j] += sg * 1e-6
+                num[j] += sg * loss(*(args[:i] + [a] + args[i + 1:])) / 2e-6
+        assert np.allclose(got[key], num, rtol=1e-6, atol=1e-7), key
+
+
+def test_norm_output_moments_and_gradients():
+    r = _rng(3)
+    x = r.normal(size=(4, 2, 7)) * 3 + 5
+    y = oracle.layer_norm(x, None, None, 0.0)
+    assert np.allclose(y.mean(-1), 0) and np.allclose((y * y).mean(-1), 1)
+    w, b = r.normal(size=(2, 7)), r.normal(size=(2, 7))
+    dO = r.normal(size=x.shape)
+    got = oracle.layer_norm_grads(x, w, dO, 1e-3)
+    for key, i in (("dx", 0), ("dweight", 1), ("dbias", 2)):
+        args = [x, w, b]
+        num = np.zeros_like(args[i])
+        for j in np.ndindex(args[i].shape):
+            for sg in (1, -1):
+                a = args[i].copy()
+                a[j] += sg * 1e-6
+                full = args[:i] + [a] + args[i + 1:]
+                num[j] += sg * (oracle.layer_norm(*full, 1e-3) * dO).sum() \
+                    / 2e-6
+        assert np.allclose(got[key], num, rtol=1e-6, atol=1e-6), key
+
+
+# ---------------------------------------------------------------- refusals
+
+def _opts(a):
+    return gdr._Opts(a["dtype"], a["gate"], a["cu"], a["nseq"], a["algo"])
+
+
+def _fwd(lib, **kw):
+    a = dict(x=A, ldx=128, la=A + STEP, s0=None, out=A + 2 * STEP,
+             sT=A + 3 * STEP, cs=None, B=2, T=64, H=2, d=64, dtype=0, gate=1,
+             cu=None, nseq=0, algo=0)
+    a.update(kw)
+    return lib.gdr_linear_fwd(a["x"], a["ldx"], a["la"], a["s0"], a["out"],
+                              a["sT"], a["cs"], a["B"], a["T"], a["H"],
+                              a["d"], None, ctypes.byref(_opts(a)))
+
+
+def _bwd(lib, **kw):
+    a = dict(x=A, ldx=128, la=A + STEP, s0=None, cs=None, dO=A + 2 * STEP,
+             dS=None, dx=A + 3 * STEP, dla=A + 4 * STEP, ds0=None, B=2, T=64,
+             H=2, d=64, dtype=0, gate=1, cu=None, nseq=0, algo=0)
+    a.update(kw)
+    return lib.gdr_linear_backward(
+        a["x"], a["ldx"], a["la"], a["s0"], a["cs"], a["dO"], a["dS"],
+        a["dx"], a["dla"], a["ds0"], a["B"], a["T"], a["H"], a["d"], None,
+        ctypes.byref(_opts(a)))
+
+
+def _step(lib, **kw):
+    a = dict(x=A, ldx=128, la=A + STEP, sin=A + 2 * STEP, sout=A + 3 * STEP,
+             out=A + 4 * STEP, N=4, H=2, d=64, dtype=0, gate=1, cu=None,
+             nseq=0, algo=0)
+    a.update(kw)
+    return lib.gdr_linear_step(a["x"], a["ldx"], a["la"], a["sin"],
+                               a["sout"], a["out"], a["N"], a["H"], a["d"],
+                               None, ctypes.byref(_opts(a)))
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd, _step])
+def test_linear_entries_reject_bad_arguments(lib, call):
+    c = lambda **kw: call(lib, **kw)  # noqa: E731
+    assert c(x=None) == INVALID
+    assert c(x=A + 8) == INVALID                   # misaligned
+    assert c(la=A + STEP + 4) == INVALID
+    assert c(la=None) == INVALID                   # a gate needs its decays
+    assert c(gate=0) == INVALID                    # ... and no gate none
+    assert c(gate=3) == INVALID
+    assert c(dtype=2) == INVALID
+    assert c(ldx=127) == INVALID                   # tokens would overlap
+    assert c(H=-1) == INVALID
+    assert c(d=0) == INVALID
+    assert c(algo=9) == INVALID
+    assert c(algo=1) == UNSUPPORTED
+    assert c(H=70000, ldx=1 << 30) == UNSUPPORTED
+    assert c(H=65535, d=65535, ldx=1 << 40) == UNSUPPORTED   # H d > 2^24
+    assert c(nseq=3) == INVALID                    # num_seqs without offsets
+
+
+def test_linear_fwd_rejects_bad_buffers(lib):
+    c = lambda **kw: _fwd(lib, **kw)  # noqa: E731
+    assert c(out=None) == INVALID
+    assert c(T=-1) == INVALID
+    assert c(cu=A, nseq=1) == INVALID              # packed needs B = 1
+    assert c(B=1, cu=A, nseq=-1) == INVALID
+    assert c(B=1, cu=A + 2, nseq=1) == INVALID
+    assert c(B=1 << 20, T=1 << 12) == UNSUPPORTED  # too many tokens
+    assert c(out=A) == INVALID                     # written over its input
+    assert c(out=A + 2 * 64 * 128 * 2 - 16) == INVALID
+    assert c(out=A + STEP) == INVALID
+    assert c(sT=A + 2 * STEP) == INVALID
+    assert c(cs=A + 2 * STEP + 16) == INVALID
+    assert c(s0=A + 3 * STEP) == INVALID
+    assert c(B=1 << 24, T=1, H=16, d=64, ldx=1024) == UNSUPPORTED  # chains
+    empty = dict(x=None, la=None, out=None, sT=None, gate=0)
+    assert c(B=0, **empty) == OK
+    assert c(H=0, **empty) == OK
+    assert c(B=1, cu=A, nseq=0, **empty) == OK
+
+
+def test_linear_backward_rejects_bad_buffers(lib, monkeypatch):
+    c = lambda **kw: _bwd(lib, **kw)  # noqa: E731
+    assert c(dO=None) == INVALID
+    assert c(dx=None) == INVALID
+    assert c(dla=None) == INVALID
+    assert c(gate=0, la=None) == INVALID           # d_log_alpha without a gate
+    assert c(dx=A) == INVALID
+    assert c(dx=A + 2 * STEP) == INVALID
+    assert c(dla=A + STEP) == INVALID
+    assert c(ds0=A + 8) == INVALID
+    assert c(cs=A + 4) == INVALID
+    assert c(dS=A + 3 * STEP) == INVALID
+    assert c(x=None, la=None, dO=None, dx=None, dla=None, gate=0, B=0) == OK
+    # the chunk states that were not given need scratch
+    monkeypatch.setenv("GDR_FAULT_INJECT_ALLOC", "1")
+    assert c() == OOM
+
+
+def test_linear_step_rejects_bad_buffers(lib):
+    c = lambda **kw: _step(lib, **kw)  # noqa: E731
+    assert c(out=None) == INVALID
+    assert c(sout=None) == INVALID
+    assert c(N=-1) == INVALID
+    assert c(cu=A, nseq=4) == INVALID
+    assert c(sout=A + 2 * STEP + 64) == INVALID    # neither in place nor apart
+    assert c(sout=A + 4 * STEP) == INVALID
+    assert c(x=None, la=None, sin=None, sout=None, out=None, gate=0,
+             N=0) == OK
+
+
+def _norm(lib, **kw):
+    a = dict(x=A, ldx=128, w=A + STEP, b=A + 2 * STEP, out=A + 3 * STEP,
+             n=8, H=2, d=64, eps=1e-5, dtype=0)
+    a.update(kw)
+    return lib.gdr_layer_norm(a["x"], a["ldx"], a["w"], a["b"], a["out"],
+                              a["n"], a["H"], a["d"], a["eps"], a["dtype"],
+                              None)
+
+
+def _norm_bwd(lib, **kw):
+    a = dict(x=A, ldx=128, w=A + STEP, dO=A + 2 * STEP, out=A + 3 * STEP,
+             dw=A + 4 * STEP, db=A + 5 * STEP, n=8, H=2, d=64, eps=1e-5,
+             dtype=0)
+    a.update(kw)
+    return lib.gdr_layer_norm_backward(
+        a["x"], a["ldx"], a["w"], a["dO"], a["out"], a["dw"], a["db"], a["n"],
+        a["H"], a["d"], a["eps"], a["dtype"], None)
+
+
+@pytest.mark.parametrize("call", [_norm, _norm_bwd])
+def test_norm_entries_reject_bad_arguments(lib, call):
+    c = lambda **kw: call(lib, **kw)  # noqa: E731
+    assert c(x=None) == INVALID
+    assert c(out=None) == INVALID
+    assert c(x=A + 2) == INVALID
+    assert c(w=A + STEP + 4) == INVALID
+    assert c(n=-1) == INVALID
+    assert c(H=-1) == INVALID
+    assert c(d=0) == INVALID
+    assert c(ldx=127) == INVALID
+    assert c(dtype=3) == INVALID
+    assert c(eps=-1e-5) == INVALID
+    assert c(eps=float("nan")) == INVALID
+    assert c(d=16385, ldx=1 << 20) == UNSUPPORTED
+    assert c(H=65536, ldx=1 << 30) == UNSUPPORTED
+    assert c(n=1 << 29, H=8, d=16) == UNSUPPORTED  # rows
+    assert c(out=A + 16) == INVALID                # overlaps
+    assert c(out=A + STEP) == INVALID
+    assert c(H=0, x=None, out=None, w=None) == OK
+
+
+def test_norm_backward_rejects_bad_buffers(lib, monkeypatch):
+    c = lambda **kw: _norm_bwd(lib, **kw)  # noqa: E731
+    assert c(dO=None) == INVALID
+    assert c(dw=A + 5 * STEP) == INVALID
+    assert c(db=A + 2 * STEP) == INVALID
+    assert c(db=A + 5 * STEP + 8) == INVALID
+    assert _norm(lib, n=0, x=None, out=None) == OK
+    monkeypatch.setenv("GDR_FAULT_INJECT_ALLOC", "1")
+    assert c() == OOM
