@@ -10,7 +10,6 @@ calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -50,7 +49,7 @@ EXPORTED_SYMBOLS = ("gdr_chunk_fwd", "gdr_chunk_fwd_host", "gdr_device_error",
 # size of the static scratch array behind gdr_chunk_fwd_noalloc
 NOALLOC_SCRATCH_BYTES = 64 << 20
 # tokens between the states that linear_fwd keeps for linear_backward
-LINEAR_CHUNK = 32
+LINEAR_CHUNK = 8
 
 _lib = None
 
@@ -604,53 +603,100 @@ def _activation(name, x, inner):
         raise ValueError(f"{name} must be a CUDA tensor")
     if x.dtype not in DTYPES:
         raise ValueError(f"{name} must be bfloat16 or float32")
+    shape = x.shape
+    outer = len(shape) - inner
     step = 1
-    shape, strides = x.shape, x.stride()
-    for i in range(x.dim() - 1, x.dim() - 1 - inner, -1):
+    if x.is_contiguous():
+        for n in shape[outer:]:
+            step *= n
+        return step
+    strides = x.stride()
+    for i in range(len(shape) - 1, outer - 1, -1):
         if shape[i] != 1 and strides[i] != step:
             raise ValueError(f"{name}: the last {inner} dimension(s) must be "
                              "contiguous")
         step *= shape[i]
     ld, rows = None, 1
-    if x.numel():
-        for i in range(x.dim() - 1 - inner, -1, -1):
-            if shape[i] == 1:
-                continue
-            if ld is None:
-                ld = strides[i]
-                if ld < step:
-                    raise ValueError(f"{name}: tokens must not overlap")
-            elif strides[i] != ld * rows:
-                raise ValueError(f"{name}: tokens must be evenly spaced")
-            rows *= shape[i]
+    for i in range(outer - 1, -1, -1):
+        if shape[i] == 1:
+            continue
+        if ld is None:
+            ld = strides[i]
+            if ld < step:
+                raise ValueError(f"{name}: tokens must not overlap")
+        elif strides[i] != ld * rows:
+            raise ValueError(f"{name}: tokens must be evenly spaced")
+        rows *= shape[i]
     return step if ld is None else ld
 
 
 def _check(name, t, shape, dtype, x):
+    """Checks another tensor of the call whose activations are x; returns its
+    address (None for None)."""
     if t is None:
-        return
+        return None
+    if (t.shape == shape and t.dtype is dtype and t.is_contiguous() and
+            t.get_device() == x.get_device()):
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, "
                          f"not {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.device != x.device:
         raise ValueError(f"{name} must be on {x.device}, not {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _on_stream(x, stream):
-    """(stream, a context to allocate and launch in): new tensors then belong
-    to that stream and the current device is x's."""
-    current = torch.cuda.current_stream(x.device)
-    if stream is None or stream == current:
-        if x.device.index == torch.cuda.current_device():
-            return current, contextlib.nullcontext()
-        return current, torch.cuda.device(x.device)
+# (the handle of the current stream without a torch.cuda.Stream around it,
+# where this build of PyTorch has it)
+_raw_stream = getattr(
+    torch._C, "_cuda_getCurrentRawStream",
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _launch(x, stream, call):
+    """call(stream handle) with x's device and the stream current, so that
+    the tensors it makes belong to that stream."""
+    if stream is None:
+        device = x.get_device()
+        if device == torch.cuda.current_device():
+            return call(_raw_stream(device))
+        with torch.cuda.device(device):
+            return call(_raw_stream(device))
     if stream.device != x.device:
         raise ValueError(f"the stream must be on {x.device}")
-    return stream, torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+_plain_opts = {}
+
+
+def _opts_of(x, gate, cu_seqlens=None):
+    if cu_seqlens is not None:
+        return _Opts(DTYPES[x.dtype], GATES[gate], cu_seqlens.data_ptr(),
+                     cu_seqlens.numel() - 1, ALGOS["auto"])
+    key = (x.dtype, gate)
+    opts = _plain_opts.get(key)
+    if opts is None:
+        opts = _plain_opts[key] = _Opts(DTYPES[x.dtype], GATES[gate], None, 0,
+                                        ALGOS["auto"])
+    return opts
+
+
+def _linear_gate(x, log_alpha, gate):
+    """(gate, address of log_alpha)"""
+    if gate is None:
+        gate = ("none" if log_alpha is None else
+                "scalar" if log_alpha.dim() == x.dim() - 1 else "channel")
+    if gate not in GATES:
+        raise ValueError(f"gate must be one of {sorted(GATES)}")
+    if (gate == "none") != (log_alpha is None):
+        raise ValueError("log_alpha must be given for a gate, and only then")
+    return gate, _check("log_alpha", log_alpha,
+                        x.shape[:-1] if gate == "scalar" else x.shape,
+                        torch.float32, x)
 
 
 def _linear_args(x, log_alpha, initial_state, gate, cu_seqlens):
@@ -666,25 +712,10 @@ def _linear_args(x, log_alpha, initial_state, gate, cu_seqlens):
             raise ValueError("cu_seqlens must be [num_seqs + 1]")
         _check("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, x)
         nseq = cu_seqlens.numel() - 1
-    g = _linear_gate(x, log_alpha, gate)
-    _check("initial_state", initial_state, (nseq, H, d), torch.float32, x)
-    opts = _Opts(DTYPES[x.dtype], GATES[g],
-                 None if cu_seqlens is None else cu_seqlens.data_ptr(),
-                 nseq if cu_seqlens is not None else 0, ALGOS["auto"])
-    return ldx, B, T, H, d, nseq, opts
-
-
-def _linear_gate(x, log_alpha, gate):
-    if gate is None:
-        gate = ("none" if log_alpha is None else
-                "scalar" if log_alpha.dim() == x.dim() - 1 else "channel")
-    if gate not in GATES:
-        raise ValueError(f"gate must be one of {sorted(GATES)}")
-    if (gate == "none") != (log_alpha is None):
-        raise ValueError("log_alpha must be given for a gate, and only then")
-    _check("log_alpha", log_alpha,
-           x.shape[:-1] if gate == "scalar" else x.shape, torch.float32, x)
-    return gate
+    g, la = _linear_gate(x, log_alpha, gate)
+    s0 = _check("initial_state", initial_state, (nseq, H, d), torch.float32,
+                x)
+    return ldx, B, T, H, d, nseq, la, s0, _opts_of(x, g, cu_seqlens)
 
 
 def linear_fwd(x, log_alpha=None, initial_state=None, *,
@@ -702,31 +733,30 @@ def linear_fwd(x, log_alpha=None, initial_state=None, *,
     to ``linear_backward``.  final_state is None if not requested.
     """
     lib = load_library()
-    ldx, B, T, H, d, nseq, opts = _linear_args(x, log_alpha, initial_state,
-                                               gate, cu_seqlens)
+    ldx, B, T, H, d, nseq, la, s0, opts = _linear_args(
+        x, log_alpha, initial_state, gate, cu_seqlens)
     _check("out", out, x.shape, x.dtype, x)
     _check("final_state", final_state, (nseq, H, d), torch.float32, x)
-    stream, on = _on_stream(x, stream)
-    with on:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if final_state is None and output_final_state:
-            final_state = torch.empty(nseq, H, d, dtype=torch.float32,
-                                      device=x.device)
-        chunk_states = None
+
+    def call(handle):
+        o = out if out is not None else x.new_empty(x.shape)
+        fin = final_state
+        if fin is None and output_final_state:
+            fin = x.new_empty((nseq, H, d), dtype=torch.float32)
+        cs = None
         if output_chunk_states:
-            chunk_states = torch.empty(B * T // LINEAR_CHUNK + nseq, H, d,
-                                       dtype=torch.float32, device=x.device)
-        rc = lib.gdr_linear_fwd(_ptr(x), ldx, _ptr(log_alpha),
-                                _ptr(initial_state), _ptr(out),
-                                _ptr(final_state), _ptr(chunk_states), B, T,
-                                H, d, ctypes.c_void_p(stream.cuda_stream),
-                                ctypes.byref(opts))
-    if rc != 0:
-        raise GdrError(rc, "gdr_linear_fwd")
-    if output_chunk_states:
-        return out, final_state, chunk_states
-    return out, final_state
+            cs = x.new_empty((B * T // LINEAR_CHUNK + nseq, H, d),
+                             dtype=torch.float32)
+        rc = lib.gdr_linear_fwd(
+            x.data_ptr(), ldx, la, s0, o.data_ptr(),
+            None if fin is None else fin.data_ptr(),
+            None if cs is None else cs.data_ptr(), B, T, H, d, handle,
+            ctypes.byref(opts))
+        if rc != 0:
+            raise GdrError(rc, "gdr_linear_fwd")
+        return (o, fin, cs) if output_chunk_states else (o, fin)
+
+    return _launch(x, stream, call)
 
 
 def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
@@ -743,26 +773,26 @@ def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
     if x.dim() != 3:
         raise ValueError("x must be [N, H, d]")
     ldx = _activation("x", x, 2)
-    N, H, d = x.shape
-    g = _linear_gate(x, log_alpha, gate)
-    _check("state", state, x.shape, torch.float32, x)
-    _check("out", out, x.shape, x.dtype, x)
-    _check("state_out", state_out, x.shape, torch.float32, x)
-    opts = _Opts(DTYPES[x.dtype], GATES[g], None, 0, ALGOS["auto"])
-    stream, on = _on_stream(x, stream)
-    with on:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if state_out is None:
-            state_out = state if state is not None else torch.empty(
-                N, H, d, dtype=torch.float32, device=x.device)
-        rc = lib.gdr_linear_step(_ptr(x), ldx, _ptr(log_alpha), _ptr(state),
-                                 _ptr(state_out), _ptr(out), N, H, d,
-                                 ctypes.c_void_p(stream.cuda_stream),
-                                 ctypes.byref(opts))
-    if rc != 0:
-        raise GdrError(rc, "gdr_linear_step")
-    return out, state_out
+    shape = x.shape
+    g, la = _linear_gate(x, log_alpha, gate)
+    sin = _check("state", state, shape, torch.float32, x)
+    _check("out", out, shape, x.dtype, x)
+    _check("state_out", state_out, shape, torch.float32, x)
+    opts = _opts_of(x, g)
+
+    def call(handle):
+        o = out if out is not None else x.new_empty(shape)
+        so = state_out if state_out is not None else state
+        if so is None:
+            so = x.new_empty(shape, dtype=torch.float32)
+        rc = lib.gdr_linear_step(x.data_ptr(), ldx, la, sin, so.data_ptr(),
+                                 o.data_ptr(), shape[0], shape[1], shape[2],
+                                 handle, ctypes.byref(opts))
+        if rc != 0:
+            raise GdrError(rc, "gdr_linear_step")
+        return o, so
+
+    return _launch(x, stream, call)
 
 
 def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
@@ -776,31 +806,37 @@ def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
     tensors dx (the dtype of x), dlog_alpha (fp32; None without a gate) and
     dinitial_state (fp32; None unless requested)."""
     lib = load_library()
-    ldx, B, T, H, d, nseq, opts = _linear_args(x, log_alpha, initial_state,
-                                               gate, cu_seqlens)
-    _check("d_out", d_out, x.shape, x.dtype, x)
-    _check("d_final_state", d_final_state, (nseq, H, d), torch.float32, x)
-    _check("chunk_states", chunk_states,
-           (B * T // LINEAR_CHUNK + nseq, H, d), torch.float32, x)
-    stream, on = _on_stream(x, stream)
-    with on:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        gla = None if log_alpha is None else torch.empty(
-            log_alpha.shape, dtype=torch.float32, device=x.device)
-        gs0 = (torch.empty(nseq, H, d, dtype=torch.float32, device=x.device)
+    ldx, B, T, H, d, nseq, la, s0, opts = _linear_args(
+        x, log_alpha, initial_state, gate, cu_seqlens)
+    do = _check("d_out", d_out, x.shape, x.dtype, x)
+    if do is None:
+        raise ValueError("d_out must be given")
+    ds = _check("d_final_state", d_final_state, (nseq, H, d), torch.float32,
+                x)
+    cs = _check("chunk_states", chunk_states,
+                (B * T // LINEAR_CHUNK + nseq, H, d), torch.float32, x)
+
+    def call(handle):
+        dx = x.new_empty(x.shape)
+        gla = None if log_alpha is None else log_alpha.new_empty(
+            log_alpha.shape)
+        gs0 = (x.new_empty((nseq, H, d), dtype=torch.float32)
                if need_initial_state_grad else None)
         rc = lib.gdr_linear_backward(
-            _ptr(x), ldx, _ptr(log_alpha), _ptr(initial_state),
-            _ptr(chunk_states), _ptr(d_out), _ptr(d_final_state), _ptr(dx),
-            _ptr(gla), _ptr(gs0), B, T, H, d,
-            ctypes.c_void_p(stream.cuda_stream), ctypes.byref(opts))
-    if rc != 0:
-        raise GdrError(rc, "gdr_linear_backward")
-    return dict(dx=dx, dlog_alpha=gla, dinitial_state=gs0)
+            x.data_ptr(), ldx, la, s0, cs, do, ds, dx.data_ptr(),
+            None if gla is None else gla.data_ptr(),
+            None if gs0 is None else gs0.data_ptr(), B, T, H, d, handle,
+            ctypes.byref(opts))
+        if rc != 0:
+            raise GdrError(rc, "gdr_linear_backward")
+        return dict(dx=dx, dlog_alpha=gla, dinitial_state=gs0)
+
+    return _launch(x, stream, call)
 
 
 def _norm_args(x, weight):
-    """(ldx, number of tokens, heads, channels, the parameters' shape)."""
+    """(ldx, number of tokens, heads, channels, the parameters' shape, the
+    weight's address)."""
     if weight is not None and weight.dim() not in (1, 2):
         raise ValueError("weight must be [d] or [H, d]")
     inner = 1 if weight is None else weight.dim()
@@ -809,12 +845,10 @@ def _norm_args(x, weight):
                          "[H, d]")
     ldx = _activation("x", x, inner)
     shape = x.shape[x.dim() - inner:]
-    _check("weight", weight, shape, torch.float32, x)
+    w = _check("weight", weight, shape, torch.float32, x)
     H, d = (1, shape[0]) if inner == 1 else shape
-    ntok = 1
-    for n in x.shape[:x.dim() - inner]:
-        ntok *= n
-    return ldx, ntok, H, d, shape
+    ntok = x.numel() // (H * d) if H * d else 0
+    return ldx, ntok, H, d, shape, w
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
@@ -827,19 +861,19 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
     lib = load_library()
     if bias is not None and weight is None:
         raise ValueError("a bias needs a weight")
-    ldx, ntok, H, d, shape = _norm_args(x, weight)
-    _check("bias", bias, shape, torch.float32, x)
+    ldx, ntok, H, d, shape, w = _norm_args(x, weight)
+    b = _check("bias", bias, shape, torch.float32, x)
     _check("out", out, x.shape, x.dtype, x)
-    stream, on = _on_stream(x, stream)
-    with on:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        rc = lib.gdr_layer_norm(_ptr(x), ldx, _ptr(weight), _ptr(bias),
-                                _ptr(out), ntok, H, d, eps, DTYPES[x.dtype],
-                                ctypes.c_void_p(stream.cuda_stream))
-    if rc != 0:
-        raise GdrError(rc, "gdr_layer_norm")
-    return out
+
+    def call(handle):
+        o = out if out is not None else x.new_empty(x.shape)
+        rc = lib.gdr_layer_norm(x.data_ptr(), ldx, w, b, o.data_ptr(), ntok,
+                                H, d, eps, DTYPES[x.dtype], handle)
+        if rc != 0:
+            raise GdrError(rc, "gdr_layer_norm")
+        return o
+
+    return _launch(x, stream, call)
 
 
 def layer_norm_backward(x, weight, d_out, *, eps: float = 1e-5,
@@ -849,23 +883,26 @@ def layer_norm_backward(x, weight, d_out, *, eps: float = 1e-5,
     Returns a dict of CUDA tensors dx (the dtype of x), dweight and dbias
     (fp32, the shape of weight; None without a weight or if not needed)."""
     lib = load_library()
-    ldx, ntok, H, d, shape = _norm_args(x, weight)
-    _check("d_out", d_out, x.shape, x.dtype, x)
-    params = need_param_grads and weight is not None
-    stream, on = _on_stream(x, stream)
-    with on:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    ldx, ntok, H, d, shape, w = _norm_args(x, weight)
+    dy = _check("d_out", d_out, x.shape, x.dtype, x)
+    if dy is None:
+        raise ValueError("d_out must be given")
+
+    def call(handle):
+        dx = x.new_empty(x.shape)
         dw = db = None
-        if params:
-            dw = torch.empty(shape, dtype=torch.float32, device=x.device)
-            db = torch.empty(shape, dtype=torch.float32, device=x.device)
+        if need_param_grads and weight is not None:
+            dw, db = weight.new_empty(shape), weight.new_empty(shape)
         rc = lib.gdr_layer_norm_backward(
-            _ptr(x), ldx, _ptr(weight), _ptr(d_out), _ptr(dx), _ptr(dw),
-            _ptr(db), ntok, H, d, eps, DTYPES[x.dtype],
-            ctypes.c_void_p(stream.cuda_stream))
-    if rc != 0:
-        raise GdrError(rc, "gdr_layer_norm_backward")
-    return dict(dx=dx, dweight=dw, dbias=db)
+            x.data_ptr(), ldx, w, dy, dx.data_ptr(),
+            None if dw is None else dw.data_ptr(),
+            None if db is None else db.data_ptr(), ntok, H, d, eps,
+            DTYPES[x.dtype], handle)
+        if rc != 0:
+            raise GdrError(rc, "gdr_layer_norm_backward")
+        return dict(dx=dx, dweight=dw, dbias=db)
+
+    return _launch(x, stream, call)
 
 
 def device_error(stream=None, clear: bool = True) -> int:

@@ -1006,7 +1006,10 @@ extern "C" gdr_status gdr_device_error(cudaStream_t stream, int clear) {
   unsigned dword = 0;   // the decode step's bulk copy never completed
   if (gdr::decode_read_error(&dword, clear != 0) != cudaSuccess)
     return GDR_ERR_CUDA;
-  if ((word & 0xFFFFFFu) || dword) return GDR_ERR_TIMEOUT;  // a wait expired
+  unsigned lword = 0;   // the linear recurrence's CTAs waited in vain
+  if (gdr::linear_read_error(&lword, clear != 0) != cudaSuccess)
+    return GDR_ERR_CUDA;
+  if ((word & 0xFFFFFFu) || dword || lword) return GDR_ERR_TIMEOUT;  // a wait expired
   return word ? GDR_ERR_RANGE : GDR_OK;
 }
 

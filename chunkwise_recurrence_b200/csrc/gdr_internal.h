@@ -93,6 +93,10 @@ cudaError_t fill_identity(float *eye, long long nstates, int dk,
 // (a bulk copy that never completed).
 cudaError_t decode_read_error(unsigned *word, bool clear);
 
+// Linear recurrence (csrc/linear.cu): reads (and optionally clears) its sticky
+// device error word (a CTA's maps that never reached another).
+cudaError_t linear_read_error(unsigned *word, bool clear);
+
 // Backward pass (csrc/backward.cu): upstream gradients in, gradients out.
 struct BackwardIO {
   const void *dout;      // dL/d out, layout of out, dtype of the problem

@@ -8,20 +8,18 @@
 // Both are scans of affine maps y -> alpha y + b, which compose:
 //   (alpha', b') o (alpha, b) = (alpha' alpha, alpha' b + b').
 //
-// One pass over the data.  A warp holds a tile of 32 tokens x 32 channels in
-// registers: a thread has V consecutive channels (one 16-byte load of fp32)
-// of R tokens in a row (R V = 32 values), scans them alone, and the
-// warp's 32 / lanes-per-row runs are joined by shuffles.  Eight warps stack
-// their tiles in time (256 tokens), and a cluster of up to 8 CTAs stacks
-// theirs; the joins travel through shared and distributed shared memory, so
-// nothing but x, log_alpha and the results touches HBM and no scratch, flag
-// or spin-wait is needed.  Each thread then runs its tokens a second time
-// from the state it now knows.
+// One pass over the data.  A thread holds 8 tokens of 4 channels in registers
+// and scans them alone; the runs of a warp (if it has more than one) are
+// joined by shuffles, those of a CTA's eight warps in shared memory, and those
+// of up to eight CTAs, stacked in time as a cluster, in distributed shared
+// memory.  Each thread then runs its tokens a second time from the state it
+// now knows.  Nothing but x, log_alpha and the results touches HBM, and there
+// is no scratch, flag or spin-wait.
 //
-// Decays near 1 are held as alpha - 1 (decay_factor): rounding alpha itself
-// to fp32 puts a systematic 2^-25 into every step, which a memory of 10^4
-// tokens turns into 3e-4.  Composed decays are sums of log_alpha until they
-// are applied, so that log_alpha = -inf clears the state exactly.
+// Decays near 1 are held as alpha - 1: rounding alpha itself to fp32 puts a
+// systematic 2^-25 into every step, which a memory of 10^4 tokens turns into
+// 3e-4.  Composed decays are sums of log_alpha until they are applied, so
+// that log_alpha = -inf clears the state exactly.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -29,21 +27,30 @@
 
 #include <climits>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 
 #include "gdr_internal.h"
+#include "sm100.cuh"
 
 namespace gdr {
+
+__device__ unsigned g_linear_error;
+
 namespace {
 
 namespace cg = cooperative_groups;
+using namespace sm100;
 
-constexpr int kTok = GDR_LINEAR_CHUNK;   // tokens of a warp's tile
-constexpr int kCh = 32;                  // channels of a warp's tile
-constexpr int kWarps = 8;
+constexpr int kV = 4;            // channels of a thread
+constexpr int kR = 8;            // tokens of a thread's run
+constexpr int kWarps = 4;        // warps of a CTA, four CTAs to an SM
 constexpr int kMaxCluster = 8;
-static_assert(kTok == 32, "a warp's tile is 32 tokens");
-
+constexpr long long kWaitCycles = 1ll << 31;   // ~1 s: never reached
+// GDR_FAULT_INJECT_LINEAR_TIMEOUT=1: no maps are sent between CTAs, and the
+// wait for them gives up after this many cycles (tests of the timeout path)
+constexpr long long kInjectWaitCycles = 1ll << 20;
+static_assert(kR == GDR_LINEAR_CHUNK, "a chunk is a run");
 struct LinParams {
   const void *x;
   const float *la, *s0;
@@ -62,71 +69,839 @@ struct LinParams {
   int tiles;        // channel tiles in all
   int nct;          // channel tiles per head; 0: tiles cut H * d as one row
   int chains;       // tiles * nseq
+  int nc;           // CTAs per chain
+  // bound of a wait for the other CTAs' maps; failure injection: none are sent
+  long long wait_cycles;
+  bool mute;
 };
 
 // ---------------------------------------------------------------- elements
 
-template <typename T, int V>
+// Four channels of a token as loaded: 16 bytes of fp32, 8 of bf16.
+template <typename T>
 struct Raw;
 template <>
-struct Raw<float, 4> { using type = float4; };
+struct Raw<float> { using type = float4; };
 template <>
-struct Raw<float, 1> { using type = float; };
-template <>
-struct Raw<__nv_bfloat16, 4> { using type = uint2; };
-template <>
-struct Raw<__nv_bfloat16, 1> { using type = unsigned short; };
+struct Raw<__nv_bfloat16> { using type = uint2; };
 
-__device__ __forceinline__ void unpack(const float4 &r, float (&f)[4]) {
+__device__ __forceinline__ void unpack(const float4 &r, float (&f)[kV]) {
   f[0] = r.x, f[1] = r.y, f[2] = r.z, f[3] = r.w;
 }
-__device__ __forceinline__ void unpack(const float &r, float (&f)[1]) {
-  f[0] = r;
-}
-__device__ __forceinline__ void unpack(const uint2 &r, float (&f)[4]) {
+__device__ __forceinline__ void unpack(const uint2 &r, float (&f)[kV]) {
   f[0] = __uint_as_float(r.x << 16), f[1] = __uint_as_float(r.x & 0xffff0000u);
   f[2] = __uint_as_float(r.y << 16), f[3] = __uint_as_float(r.y & 0xffff0000u);
-}
-__device__ __forceinline__ void unpack(const unsigned short &r,
-                                       float (&f)[1]) {
-  f[0] = __uint_as_float((unsigned)r << 16);
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&p);
 }
-__device__ __forceinline__ void store(float *p, const float (&f)[4]) {
-  *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+// Forgets what the compiler knows about a loaded value, so that it does not
+// keep the unpacked elements in registers from one pass to the next.
+__device__ __forceinline__ void renew(uint2 &r) {
+  asm volatile("" : "+r"(r.x), "+r"(r.y));
 }
-__device__ __forceinline__ void store(float *p, const float (&f)[1]) {
-  *p = f[0];
+__device__ __forceinline__ void renew(float4 &) {}
+
+// A thread's first n <= 4 channels, as one vector (VEC: n is 4 or 0) or one
+// by one where rows are not aligned for that.
+template <bool VEC>
+__device__ __forceinline__ void store(float *p, const float (&f)[kV], int n) {
+  if constexpr (VEC) {
+    if (n > 0)
+      *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+      if (n > v) p[v] = f[v];
+  }
 }
-__device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[4]) {
-  *reinterpret_cast<uint2 *>(p) =
-      make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+template <bool VEC>
+__device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[kV],
+                                      int n) {
+  if constexpr (VEC) {
+    if (n > 0)
+      *reinterpret_cast<uint2 *>(p) =
+          make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+  } else {
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+      if (n > v) p[v] = __float2bfloat16_rn(f[v]);
+  }
 }
-__device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[1]) {
-  *p = __float2bfloat16_rn(f[0]);
+
+// Asynchronous copy of `bytes` <= N bytes (N = 4, 8 or 16) into N bytes of
+// shared memory; the rest is zero and not read.
+template <int N>
+__device__ __forceinline__ void copy_async(void *dst, const void *src,
+                                           int bytes) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d),
+                 "l"(src), "n"(N), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_landed() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Two fp32 values in a register pair, for the instructions that work on both
+// at once.
+struct Pair {
+  unsigned long long u;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.u) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ void split(Pair p, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p.u));
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+  return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(a.u), "l"(b.u));
+  return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(a.u), "l"(b.u));
+  return d;
 }
 
 // ------------------------------------------------------------------ decays
 
-// The decay e^s in the form the state is multiplied by: for -1/8 < s <= 0
-// (sign bit set, also at s = 0) the value is e^s - 1 to its own relative
-// precision, by its Taylor series (the first term left out is under 5e-8 of
-// the sum); elsewhere (sign bit clear) it is e^s.
-__device__ __forceinline__ float decay_factor(float s) {
-  float p = fmaf(s, 1.f / 120.f, 1.f / 24.f);
-  p = fmaf(s, p, 1.f / 6.f);
-  p = fmaf(s, p, 0.5f);
-  p = fmaf(s, p, 1.f);
-  const float near1 = -fabsf(s) * p;
-  const float far1 = __expf(s);
-  return (s > -0.125f && s <= 0.f) ? near1 : far1;
+// e^x, results below 2^-126 as 0
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
 }
-// e^s h, from decay_factor(s)
+// e^s - 1 for kTight <= s <= 0: s times a least-maximum-error polynomial of
+// (e^s - 1) / s (fitted by reweighted least squares; off by 1.4e-7 of e^s - 1
+// at most, evaluated in fp32, and exact for s -> 0)
+constexpr float kTight = -1.f;
+__device__ __forceinline__ float expm1_tight(float s) {
+  float p = fmaf(s, 1.283806487e-4f, 1.298663556e-3f);
+  p = fmaf(s, p, 8.273095824e-3f);
+  p = fmaf(s, p, 4.164557904e-2f);
+  p = fmaf(s, p, 1.666630954e-1f);
+  p = fmaf(s, p, 4.999997616e-1f);
+  p = fmaf(s, p, 1.f);
+  return s * p;
+}
+
+__device__ __forceinline__ Pair expm1_tight(Pair s) {
+  Pair p = fma2(s, pair(1.283806487e-4f, 1.283806487e-4f),
+                pair(1.298663556e-3f, 1.298663556e-3f));
+  p = fma2(s, p, pair(8.273095824e-3f, 8.273095824e-3f));
+  p = fma2(s, p, pair(4.164557904e-2f, 4.164557904e-2f));
+  p = fma2(s, p, pair(1.666630954e-1f, 1.666630954e-1f));
+  p = fma2(s, p, pair(4.999997616e-1f, 4.999997616e-1f));
+  p = fma2(s, p, pair(1.f, 1.f));
+  return mul2(s, p);
+}
+
+// The decay e^s in one of two forms.  Tight (kTight <= s <= 0, the usual
+// decays): e^s - 1.  Any: for -1/8 < s <= 0 (sign bit set, also at s = 0)
+// e^s - 1, else (sign bit clear) e^s, right to its own precision however
+// small; dearer to make and to apply.
+template <bool TIGHT>
+__device__ __forceinline__ float decay_factor(float s) {
+  if constexpr (TIGHT) return expm1_tight(s);
+  return s > -0.125f && s <= 0.f ? -fabsf(expm1_tight(s)) : exp_fast(s);
+}
+// e^s h, from decay_factor<TIGHT>(s)
+template <bool TIGHT>
 __device__ __forceinline__ float decay(float m, float h) {
+  if constexpr (TIGHT) return fmaf(m, h, h);
   return fmaf(m, h, __float_as_int(m) < 0 ? h : 0.f);
+}
+template <int GATE, bool TIGHT>
+__device__ __forceinline__ float decayed(float m, float h) {
+  if constexpr (GATE == GDR_GATE_NONE) return h;
+  return decay<TIGHT>(m, h);
+}
+// y <- e^s y + x over a thread's channels, from their factors m
+template <int GV, int GATE, bool TIGHT>
+__device__ __forceinline__ void advance(float (&y)[kV], const float (&m)[GV],
+                                        const float (&x)[kV]) {
+  if constexpr (TIGHT) {
+#pragma unroll
+    for (int v = 0; v < kV; v += 2) {
+      Pair h = pair(y[v], y[v + 1]);
+      if constexpr (GATE != GDR_GATE_NONE)
+        h = fma2(pair(m[GV == kV ? v : 0], m[GV == kV ? v + 1 : 0]), h, h);
+      split(add2(h, pair(x[v], x[v + 1])), y[v], y[v + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+      y[v] = decayed<GATE, false>(m[GV == kV ? v : 0], y[v]) + x[v];
+  }
+}
+// y <- e^s y
+template <int GV, int GATE, bool TIGHT>
+__device__ __forceinline__ void decay_all(float (&y)[kV],
+                                          const float (&m)[GV]) {
+  if constexpr (GATE == GDR_GATE_NONE) return;
+  if constexpr (TIGHT) {
+#pragma unroll
+    for (int v = 0; v < kV; v += 2) {
+      const Pair h = pair(y[v], y[v + 1]);
+      split(fma2(pair(m[GV == kV ? v : 0], m[GV == kV ? v + 1 : 0]), h, h),
+            y[v], y[v + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+      y[v] = decayed<GATE, false>(m[GV == kV ? v : 0], y[v]);
+  }
+}
+__device__ __forceinline__ void add_all(float (&y)[kV], const float (&x)[kV]) {
+#pragma unroll
+  for (int v = 0; v < kV; v += 2)
+    split(add2(pair(y[v], y[v + 1]), pair(x[v], x[v + 1])), y[v], y[v + 1]);
+}
+// One token's log-decays into factors, added to the run's sums.
+template <int GV, int GATE, bool TIGHT>
+__device__ __forceinline__ void factors(float (&m)[GV], float (&sum)[GV]) {
+  if constexpr (GATE == GDR_GATE_NONE) return;
+  if constexpr (TIGHT && GV == kV) {
+#pragma unroll
+    for (int v = 0; v < GV; v += 2) {
+      const Pair s = pair(m[v], m[v + 1]);
+      split(add2(pair(sum[v], sum[v + 1]), s), sum[v], sum[v + 1]);
+      split(expm1_tight(s), m[v], m[v + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < GV; ++v) {
+      sum[v] += m[v];
+      m[v] = decay_factor<TIGHT>(m[v]);
+    }
+  }
+}
+
+// the map (s, b): y -> e^s y + b
+template <int GATE, bool TIGHT = false>
+__device__ __forceinline__ float apply(float2 m, float y) {
+  if constexpr (GATE == GDR_GATE_NONE) return y + m.y;
+  return decay<TIGHT>(decay_factor<TIGHT>(m.x), y) + m.y;
+}
+
+template <bool B>
+struct Bool { static constexpr bool value = B; };
+
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float y;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Whether every log-decay the warp holds is tight.
+template <int GV, int GATE>
+__device__ __forceinline__ bool is_tight(const float (&s)[kR][GV]) {
+  if constexpr (GATE == GDR_GATE_NONE) return true;
+  float lo = 0.f, hi = 0.f;
+#pragma unroll
+  for (int r = 0; r < kR; r += 2)
+#pragma unroll
+    for (int v = 0; v < GV; ++v) {
+      lo = min3(lo, s[r][v], s[r + 1][v]);
+      hi = max3(hi, s[r][v], s[r + 1][v]);
+    }
+  return __all_sync(~0u, lo >= kTight && hi <= 0.f);
+}
+// The same for its runs' sums, given that each decay is.
+template <int GV, int GATE>
+__device__ __forceinline__ bool is_tight_run(const float (&s)[GV], bool each) {
+  if constexpr (GATE == GDR_GATE_NONE) return true;
+  float lo = s[0];
+#pragma unroll
+  for (int v = 1; v < GV; ++v) lo = fminf(lo, s[v]);
+  return __all_sync(~0u, each && lo >= kTight);
+}
+
+// ------------------------------------------------------------------- tiles
+
+// A warp's tile: kLanes threads side by side over 4 kLanes channels, and
+// kSubs = 32 / kLanes runs of 8 tokens.
+template <int LANES, int GATE>
+struct Tile {
+  static constexpr int kCh = kV * LANES;
+  static constexpr int kSubs = 32 / LANES;
+  static constexpr int kTok = kR * kSubs;
+  // decays per thread and token (a thread's channels share a scalar one)
+  static constexpr int GV = GATE == GDR_GATE_CHANNEL ? kV : 1;
+};
+
+template <int GV>
+struct Map {       // y -> e^s y + b per channel of a thread
+  float s[GV], b[kV];
+};
+
+// Scan of the warp's runs, in time (REV = false) or against it: on return
+// `f` maps over this run and all before it (in scan order), `ex` over those
+// before it alone.
+template <int LANES, int GV, int GATE, bool REV>
+__device__ __forceinline__ void warp_scan(Map<GV> &f, Map<GV> &ex,
+                                          bool tight) {
+  if constexpr (LANES < 32) {
+    const int lane = threadIdx.x & 31;
+    auto from = [](float x, int off) {
+      return REV ? __shfl_down_sync(~0u, x, off) : __shfl_up_sync(~0u, x, off);
+    };
+    auto stage = [&](int off, auto tc) {
+      const bool has = REV ? lane + off < 32 : lane >= off;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        const float gb = from(f.b[v], off);
+        const float y = apply<GATE, tc.value>(
+            make_float2(f.s[GV == kV ? v : 0], f.b[v]), gb);
+        if (has) f.b[v] = y;
+      }
+#pragma unroll
+      for (int v = 0; v < GV; ++v) {
+        const float gs = from(f.s[v], off);
+        if (has) f.s[v] += gs;
+      }
+    };
+    if (tight) stage(LANES, Bool<true>{}); else stage(LANES, Bool<false>{});
+    if constexpr (LANES < 16) stage(2 * LANES, Bool<false>{});
+    const bool first = REV ? lane + LANES >= 32 : lane < LANES;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const float b = from(f.b[v], LANES);
+      ex.b[v] = first ? 0.f : b;
+    }
+#pragma unroll
+    for (int v = 0; v < GV; ++v) {
+      const float s = from(f.s[v], LANES);
+      ex.s[v] = first ? 0.f : s;
+    }
+  }
+}
+// y, the value that enters the warp's tile, moved on to this thread's run.
+template <int LANES, int GV, int GATE>
+__device__ __forceinline__ void enter(float (&y)[kV], const Map<GV> &ex,
+                                      bool tight) {
+  if constexpr (LANES < 32) {
+    auto go = [&](auto tc) {
+#pragma unroll
+      for (int v = 0; v < kV; ++v)
+        y[v] = apply<GATE, tc.value>(
+            make_float2(ex.s[GV == kV ? v : 0], ex.b[v]), y[v]);
+    };
+    // (two runs per warp: `ex` is one run's map)
+    if (LANES == 16 && tight) go(Bool<true>{}); else go(Bool<false>{});
+  }
+}
+
+// A thread's place: its sequence, its channels.
+struct Place {
+  int n;            // sequence
+  int base, end;    // channels of the tile: [base, min(base + CH, end))
+  int ch, nch;      // the thread's first channel, and how many it has
+  int head, ct;     // the tile's head and tile within it (nct > 0)
+};
+template <int LANES>
+__device__ __forceinline__ Place place(const LinParams &p, int chain) {
+  Place q;
+  const int c = (threadIdx.x & 31) % LANES;
+  const int tile = chain % p.tiles;
+  q.n = chain / p.tiles;
+  q.head = q.ct = 0;
+  if (p.nct) {
+    q.head = tile / p.nct;
+    q.ct = tile - q.head * p.nct;
+    q.base = q.head * p.d + q.ct * kV * LANES;
+    q.end = (q.head + 1) * p.d;
+  } else {
+    q.base = tile * kV * LANES;
+    q.end = p.D;
+  }
+  q.ch = q.base + c * kV;
+  q.nch = min(max(q.end - q.ch, 0), kV);
+  return q;
+}
+
+// The inputs of one step where rows are aligned for vectors: a thread's own 8
+// tokens of 4 channels are fetched into the thread's own slots of shared
+// memory while the step before is computed.  Slots are [token][thread], so
+// that a warp's accesses are contiguous; nobody else reads them.
+template <typename T, int GATE, bool BWD>
+struct Slots {
+  using raw_t = typename Raw<T>::type;
+  static constexpr bool kX = !BWD || GATE != GDR_GATE_NONE;
+  static constexpr int GV = GATE == GDR_GATE_CHANNEL ? kV : 1;
+  static constexpr bool kGate = GATE == GDR_GATE_CHANNEL;
+  static constexpr bool kState = BWD && GATE != GDR_GATE_NONE;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kSlots = kR * kThreads;
+  static constexpr int kRaw = (int)sizeof(raw_t);
+  static constexpr int kBytes =
+      kSlots * (16 * kGate + kRaw * (kX + BWD)) + 16 * kThreads * kState;
+  // at the thread's first token of the step to fetch; distances between
+  // tokens, in elements
+  const T *x, *dout;
+  const float *la, *states;
+  int ldx, ldg, ldd;
+  bool has;                // whether the thread has channels (4 or none)
+  float sc[kR];            // scalar decays of the step to come
+
+  __device__ __forceinline__ void start(const LinParams &p, const Place &q,
+                                        int tok0, int t) {
+    ldx = (int)p.ldx;
+    ldg = GATE == GDR_GATE_SCALAR ? p.H : p.D;
+    ldd = p.D;
+    has = q.nch > 0;
+    const long long tok = (long long)tok0 + t;
+    x = static_cast<const T *>(p.x) + tok * ldx + q.ch;
+    dout = static_cast<const T *>(p.dout) + tok * ldd + q.ch;
+    la = p.la + tok * ldg +
+         (GATE == GDR_GATE_CHANNEL ? q.ch : p.nct ? q.head : q.ch / p.d);
+    // (t is a multiple of 8, and so is what it moves on by)
+    states = p.states + ((long long)(tok0 / kR) + q.n + t / kR) * ldd + q.ch;
+  }
+  __device__ __forceinline__ void move(int tokens) {
+    x += (long long)tokens * ldx;
+    la += (long long)tokens * ldg;
+    if constexpr (BWD) {
+      dout += (long long)tokens * ldd;
+      states += (long long)(tokens / kR) * ldd;
+    }
+  }
+
+  static __device__ __forceinline__ raw_t *xs(char *sm) {
+    return reinterpret_cast<raw_t *>(sm) + threadIdx.x;
+  }
+  static __device__ __forceinline__ raw_t *ds(char *sm) {
+    return xs(sm) + (kX ? kSlots : 0);
+  }
+  static __device__ __forceinline__ float4 *gs(char *sm) {
+    return reinterpret_cast<float4 *>(sm + kSlots * kRaw * (kX + BWD)) +
+           threadIdx.x;
+  }
+  // sends for the 8 tokens from t on, those before `end`
+  template <bool FULL>
+  __device__ __forceinline__ void send_all(char *sm, int t, int end) {
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const bool ok = FULL || (t + r < end && has);
+      if constexpr (!BWD)
+        copy_async<kRaw>(xs(sm) + r * kThreads, x + (long long)r * ldx,
+                         ok ? kRaw : 0);
+      if constexpr (BWD)
+        copy_async<kRaw>(ds(sm) + r * kThreads, dout + (long long)r * ldd,
+                         ok ? kRaw : 0);
+      if constexpr (kGate)
+        copy_async<16>(gs(sm) + r * kThreads, la + (long long)r * ldg,
+                       ok ? 16 : 0);
+    }
+    if constexpr (kState)
+      copy_async<16>(gs(sm) + kSlots * kGate, states,
+                     t < end && has ? 16 : 0);
+  }
+  __device__ __forceinline__ void fetch(char *sm, int t, int end) {
+    if constexpr (GATE == GDR_GATE_SCALAR) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+        sc[r] = t + r < end && has ? __ldg(la + (long long)r * ldg) : 0.f;
+    }
+    if (!BWD && t + kR <= end && has)
+      send_all<true>(sm, t, end);
+    else
+      send_all<false>(sm, t, end);
+  }
+  // x of the backward pass comes on its own: it is read where it is used, to
+  // spare registers, and so is still in its slots when the rest is fetched
+  __device__ __forceinline__ void fetch_x(char *sm, const T *at, int t,
+                                          int end) const {
+    if constexpr (BWD && kX) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+        copy_async<kRaw>(xs(sm) + r * kThreads, at + (long long)r * ldx,
+                         t + r < end && has ? kRaw : 0);
+    }
+  }
+  __device__ __forceinline__ raw_t x_at(char *sm, int r) const {
+    return xs(sm)[r * kThreads];
+  }
+  __device__ __forceinline__ void take(char *sm, raw_t (&xr)[kR],
+                                       raw_t (&dr)[kR], float (&m)[kR][GV],
+                                       float (&h)[kV]) const {
+    copies_landed();
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      if constexpr (!BWD) xr[r] = x_at(sm, r);
+      if constexpr (BWD) dr[r] = ds(sm)[r * kThreads];
+      if constexpr (kGate) unpack(gs(sm)[r * kThreads], m[r]);
+      if constexpr (GATE == GDR_GATE_SCALAR) m[r][0] = sc[r];
+    }
+    if constexpr (kState) unpack(gs(sm)[kSlots * kGate], h);
+  }
+};
+
+// The inputs and results of one step where rows are not aligned: a warp's
+// tile of 32 tokens by 32 channels goes through shared memory row by row, a
+// lane to a channel (of bf16, a lane to a 4-byte word, since a row may start
+// in the middle of one), and from there to the threads that compute it and
+// back.  Nothing is fetched ahead.
+template <typename T, int GATE, bool BWD>
+struct Rows {
+  using raw_t = typename Raw<T>::type;
+  static constexpr bool kX = !BWD || GATE != GDR_GATE_NONE;
+  static constexpr int GV = GATE == GDR_GATE_CHANNEL ? kV : 1;
+  static constexpr bool kGate = GATE == GDR_GATE_CHANNEL;
+  static constexpr bool kState = BWD && GATE != GDR_GATE_NONE;
+  static constexpr int kRow = 32;                      // tokens and channels
+  // words of a row in shared memory: of bf16 16, and one for an odd start
+  static constexpr int kPitch = sizeof(T) == 4 ? 32 : 17;
+  static constexpr int kTile = kRow * kPitch * 4;      // of x or dout
+  static constexpr int kTileG = kGate ? kRow * 32 * 4 : 0;
+  static constexpr int kTileS = kState ? 4 * 32 * 4 : 0;
+  static constexpr int kWarp = kTile * (kX + BWD) + kTileG + kTileS;
+  static constexpr int kBytes = kWarp * kWarps;
+  // at the tile's first channel of the sequence's first token
+  const T *x, *dout;
+  const float *la, *states;
+  T *out;
+  float *dla;
+  int ldx, ldg, ldd, n;    // n: channels of the tile that exist
+  int t0, end;             // the tile's tokens: t0 .. t0 + 31, those < end
+  int tn, endn;            // of the step to come
+
+  __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
+  __device__ __forceinline__ int sub() const { return lane() / 8; }
+  __device__ __forceinline__ int col() const { return lane() % 8; }
+
+  __device__ __forceinline__ void start(const LinParams &p, const Place &q,
+                                        int tok0, int) {
+    ldx = (int)p.ldx;
+    ldg = GATE == GDR_GATE_SCALAR ? p.H : p.D;
+    ldd = p.D;
+    n = min(q.end - q.base, kRow);
+    x = static_cast<const T *>(p.x) + (long long)tok0 * ldx + q.base;
+    dout = static_cast<const T *>(p.dout) + (long long)tok0 * ldd + q.base;
+    la = p.la + (long long)tok0 * ldg +
+         (GATE == GDR_GATE_CHANNEL ? q.base : q.head);
+    states = p.states + ((long long)(tok0 / kR) + q.n) * ldd + q.base;
+    out = static_cast<T *>(BWD ? p.dx : p.out) + (long long)tok0 * ldd +
+          q.base;
+    dla = p.dla + (long long)tok0 * ldd + q.base;
+  }
+  __device__ __forceinline__ void move(int) {}
+  __device__ __forceinline__ void fetch(char *, int t, int e) {
+    tn = t - sub() * kR;
+    endn = e;
+    if (tn + lane() < e) {
+      if constexpr (kX) soon(x, ldx);
+      if constexpr (BWD) soon(dout, ldd);
+      if constexpr (kGate) soon(la, ldg);
+    }
+  }
+  __device__ __forceinline__ void fetch_x(char *, const T *, int, int) const {}
+
+  __device__ __forceinline__ char *base(char *sm) const {
+    return sm + (threadIdx.x >> 5) * kWarp;
+  }
+  __device__ __forceinline__ char *ds(char *sm) const {
+    return base(sm) + (kX ? kTile : 0);
+  }
+  __device__ __forceinline__ float *gs(char *sm) const {
+    return reinterpret_cast<float *>(base(sm) + kTile * (kX + BWD));
+  }
+  // ROWS rows of fp32, the first `have` of them
+  template <int ROWS>
+  __device__ __forceinline__ void rows(float *dst, const float *src, int ld,
+                                       int have) const {
+    src += lane();
+    dst += lane();
+    if (lane() >= n) have = 0;
+    float v[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      v[r] = 0.f;
+      if (r < have) v[r] = __ldg(src + (long long)r * ld);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) dst[r * 32] = v[r];
+  }
+  // the same of bf16, two rows at a time; a lane's rows all start alike.  Of
+  // a word whose second half is beyond the tile only the first is read.
+  template <int ROWS>
+  __device__ __forceinline__ void rows(float *dst, const __nv_bfloat16 *src,
+                                       int ld, int have) const {
+    auto word = [&](int r, int j, int &bytes) {
+      const uintptr_t at =
+          reinterpret_cast<uintptr_t>(src + (long long)r * ld);
+      bytes = (int)(at & 2) + 2 * n - 4 * j;
+      return reinterpret_cast<const char *>(at & ~(uintptr_t)3) + 4 * j;
+    };
+    auto read = [&](const char *p, bool ok, int bytes) {
+      uint32_t v = 0;
+      if (ok && bytes >= 4) v = __ldg(reinterpret_cast<const uint32_t *>(p));
+      if (ok && bytes == 2)
+        v = __ldg(reinterpret_cast<const unsigned short *>(p));
+      return __uint_as_float(v);
+    };
+    const int r0 = lane() / 16, j = lane() % 16;
+    int bytes, bytes1;
+    const char *p = word(r0, j, bytes);
+    const char *p1 = word(lane(), 16, bytes1);
+    float v[ROWS / 2];
+#pragma unroll
+    for (int r = 0; r < ROWS; r += 2)
+      v[r / 2] = read(p + (long long)r * (2 * ld), r + r0 < have, bytes);
+    const float v1 = read(p1, lane() < have, bytes1);
+    float *d = dst + r0 * kPitch + j;
+#pragma unroll
+    for (int r = 0; r < ROWS; r += 2) d[r * kPitch] = v[r / 2];
+    dst[lane() * kPitch + 16] = v1;
+  }
+  // brings row `lane` of the next step's tile into L2
+  template <typename E>
+  __device__ __forceinline__ void soon(const E *src, int ld) const {
+    const E *row = src + (long long)(tn + lane()) * ld;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(row) : "memory");
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(row + n - 1) : "memory");
+  }
+  // the thread's 4 channels of its token r, of the tile that starts at `src`
+  // (a tile's first token has an even index, and so has each thread's)
+  __device__ __forceinline__ raw_t at(const char *tile, const T *src, int ld,
+                                      int r) const {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(tile) +
+                        (sub() * kR + r) * kPitch;
+    if constexpr (sizeof(T) == 4) {
+      return *reinterpret_cast<const float4 *>(w + col() * 4);
+    } else {
+      w += col() * 2;
+      const bool odd =
+          (((int)reinterpret_cast<uintptr_t>(src) >> 1) ^ (r & ld)) & 1;
+      return odd ? make_uint2(__funnelshift_r(w[0], w[1], 16),
+                              __funnelshift_r(w[1], w[2], 16))
+                 : make_uint2(w[0], w[1]);
+    }
+  }
+  __device__ __forceinline__ raw_t x_at(char *sm, int r) const {
+    return at(base(sm), x, ldx, r);
+  }
+  __device__ __forceinline__ void take(char *sm, raw_t (&xr)[kR],
+                                       raw_t (&dr)[kR], float (&m)[kR][GV],
+                                       float (&h)[kV]) {
+    t0 = tn;
+    end = endn;
+    const int have = end > t0 ? min(end - t0, kRow) : 0;
+    const long long at0 = have > 0 ? t0 : 0;
+    __syncwarp();          // the step before is out of shared memory
+    if constexpr (kX)
+      rows<kRow>(reinterpret_cast<float *>(base(sm)), x + at0 * ldx, ldx,
+                 have);
+    if constexpr (BWD)
+      rows<kRow>(reinterpret_cast<float *>(ds(sm)), dout + at0 * ldd, ldd,
+                 have);
+    if constexpr (kGate) rows<kRow>(gs(sm), la + at0 * ldg, ldg, have);
+    if constexpr (kState)
+      rows<4>(gs(sm) + kTileG / 4, states + at0 / kR * ldd, ldd,
+              (have + kR - 1) / kR);
+    if constexpr (GATE == GDR_GATE_SCALAR) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        const int row = sub() * kR + r;
+        m[r][0] = row < have ? __ldg(la + (at0 + row) * ldg) : 0.f;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      if constexpr (!BWD) xr[r] = x_at(sm, r);
+      if constexpr (BWD) dr[r] = at(ds(sm), dout, ldd, r);
+      if constexpr (kGate)
+        unpack(*reinterpret_cast<const float4 *>(
+                   gs(sm) + (sub() * kR + r) * 32 + col() * 4),
+               m[r]);
+    }
+    if constexpr (kState)
+      unpack(*reinterpret_cast<const float4 *>(gs(sm) + kTileG / 4 +
+                                               sub() * 32 + col() * 4),
+             h);
+    __syncwarp();          // the tiles of dout (x) and of the decays are free
+  }
+  // results: into the tiles of dout (forward: x) and of the decays ...
+  __device__ __forceinline__ void put(char *sm, int r, const float (&f)[kV]) {
+    T *d = reinterpret_cast<T *>(BWD ? ds(sm) : base(sm));
+    store<true>(d + (sub() * kR + r) * kRow + col() * kV, f, kV);
+  }
+  __device__ __forceinline__ void put_la(char *sm, int r,
+                                         const float (&f)[kV]) {
+    store<true>(gs(sm) + (sub() * kR + r) * kRow + col() * kV, f, kV);
+  }
+  // ... and out, row by row
+  __device__ __forceinline__ void flush(char *sm) {
+    const T *d = reinterpret_cast<const T *>(BWD ? ds(sm) : base(sm)) + lane();
+    const float *g = gs(sm) + lane();
+    const int have = lane() < n ? min(end - t0, kRow) : 0;
+    T *o = out + (long long)t0 * ldd + lane();
+    float *og = dla + (long long)t0 * ldd + lane();
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kRow; ++r)
+      if (r < have) {
+        o[(long long)r * ldd] = d[r * kRow];
+        if constexpr (BWD && kGate) og[(long long)r * ldd] = g[r * kRow];
+      }
+  }
+};
+
+template <typename T, bool VEC, int GATE, bool BWD>
+struct InputsOf { using type = Rows<T, GATE, BWD>; };
+template <typename T, int GATE, bool BWD>
+struct InputsOf<T, true, GATE, BWD> { using type = Slots<T, GATE, BWD>; };
+template <typename T, bool VEC, int GATE, bool BWD>
+using Inputs = typename InputsOf<T, VEC, GATE, BWD>::type;
+
+// The joins across the warps of a CTA and the CTAs of a cluster.
+template <int CH, int NW>
+struct __align__(128) Joint {
+  float2 warp[NW][CH];                   // each warp's map
+  float in[NW][CH];                      // what enters each warp's tile
+  float2 rank[2][kMaxCluster][CH];       // each CTA's map; alternating, since
+                                         // a CTA may be a step ahead
+  uint64_t full[2];                      // mbarriers: a step's maps are here
+};
+
+// --- exchange between the CTAs of a cluster.  A map goes to every CTA as an
+// asynchronous remote store that counts its bytes down on the receiver's
+// mbarrier: no cluster-wide barrier (whose release would wait for all the
+// results still on their way to memory) in the loop.  Bytes for step k + 2
+// cannot arrive before step k was read: their sender has first received step
+// k + 1 from this CTA, which sends it after that reading.
+__device__ __forceinline__ uint32_t remote(const void *p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(a)
+      : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void send_map(uint32_t dst, float2 m,
+                                         uint32_t bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], "
+      "{%1, %2}, [%3];" ::"r"(dst),
+      "f"(m.x), "f"(m.y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool maps_here(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
+      "%2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+
+// Every warp's map into shared memory (`edge`: this thread's run holds it).
+template <int GV, int GATE, typename J>
+__device__ __forceinline__ void post(J &jt, const Map<GV> &f, int c,
+                                     bool edge) {
+  const int w = threadIdx.x >> 5;
+  if (edge) {
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+      jt.warp[w][c * kV + v] =
+          make_float2(GATE == GDR_GATE_NONE ? 0.f : f.s[GV == kV ? v : 0],
+                      f.b[v]);
+  }
+  __syncthreads();
+}
+
+// Runs the posted maps: thread i < CH looks after channel i and carries its
+// value (`carry`) from step to step.  Leaves jt.in for everyone.
+template <int CH, int GATE, bool REV, bool CL, typename J>
+__device__ __forceinline__ void run_maps(J &jt, int step, int nc, int rank,
+                                         long long &limit, bool mute,
+                                         float &carry) {
+  const int i = threadIdx.x, buf = step & 1;
+  if constexpr (!CL) {
+    if (i < CH) {
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const int j = REV ? kWarps - 1 - k : k;
+        jt.in[j][i] = carry;
+        carry = apply<GATE>(jt.warp[j][i], carry);
+      }
+    }
+  } else {
+    float2 pre[kWarps];                  // the maps of the warps before
+    if (i < CH) {
+      // (after an expired wait nothing more is sent, expected or waited for)
+      if (i == 0 && limit > 0)
+        mbar_arrive_expect_tx(&jt.full[buf], nc * CH * (int)sizeof(float2));
+      float2 m = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float2 g = jt.warp[REV ? kWarps - 1 - k : k][i];
+        pre[k] = m;
+        m = make_float2(m.x + g.x, apply<GATE>(g, m.y));
+      }
+      if (!mute && limit > 0)
+        for (int r = 0; r < nc; ++r)
+          send_map(remote(&jt.rank[buf][rank][i], r), m,
+                   remote(&jt.full[buf], r));
+      // bounded: after one wait that expires no other is waited for, so that
+      // every CTA gets to the end, where the cluster meets once more
+      if (limit > 0) {
+        const long long start = clock64();
+        while (!maps_here(&jt.full[buf], (step >> 1) & 1))
+          if (clock64() - start > limit) {
+            limit = 0;
+            atomicExch(&g_linear_error, 1u);
+            break;
+          }
+      }
+      float y = 0.f;
+      for (int r = 0; r < nc; ++r) {
+        if (r == rank) y = carry;
+        carry = apply<GATE>(jt.rank[buf][r][i], carry);
+      }
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+        jt.in[REV ? kWarps - 1 - k : k][i] = apply<GATE>(pre[k], y);
+    }
+  }
+  __syncthreads();
+}
+
+// No CTA writes into another's shared memory before that one has begun and
+// set up its mbarriers (nor after it has ended: the kernels end with another
+// meeting).
+template <typename J>
+__device__ __forceinline__ void meet_first(J &jt) {
+  if (threadIdx.x == 0) {
+    mbar_init(&jt.full[0], 1);
+    mbar_init(&jt.full[1], 1);
+    fence_mbar_init();
+  }
+  cg::this_cluster().sync();
 }
 
 // Tokens [*a, *a + *len) of sequence n.  Offsets that do not lie in order
@@ -145,505 +920,293 @@ __device__ __forceinline__ void seq_range(const LinParams &p, int n, int *a,
   }
 }
 
-// What a warp's threads hold of one tile, and the joins inside the warp.
-template <int V, int GATE>
-struct Tile {
-  static constexpr int kLanes = kCh / V;         // threads per token
-  static constexpr int kSubs = 32 / kLanes;      // token runs per warp
-  static constexpr int R = kTok / kSubs;         // tokens per run
-  static constexpr int GV = GATE == GDR_GATE_CHANNEL ? V : 1;
-};
-
-template <int V, int GV>
-struct Map {       // y -> e^s y + b per channel
-  float s[GV], b[V];
-};
-
-// this = this o other (other is applied first)
-template <int V, int GV, int GATE>
-__device__ __forceinline__ void after(Map<V, GV> &f, const Map<V, GV> &g) {
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if constexpr (GATE == GDR_GATE_NONE) {
-      f.b[v] += g.b[v];
-    } else {
-      f.b[v] += decay(decay_factor(f.s[GV == V ? v : 0]), g.b[v]);
-    }
-  }
-  if constexpr (GATE != GDR_GATE_NONE)
-#pragma unroll
-    for (int v = 0; v < GV; ++v) f.s[v] += g.s[v];
-}
-
-// Scan of the warp's runs, in time (REV = false) or against it: on return
-// `f` maps over this run and all before it (in scan order), `ex` over those
-// before it alone.
-template <int V, int GV, int GATE, bool REV>
-__device__ __forceinline__ void warp_scan(Map<V, GV> &f, Map<V, GV> &ex) {
-  constexpr int L = kCh / V;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int off = L; off < 32; off <<= 1) {
-    Map<V, GV> g;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      g.b[v] = REV ? __shfl_down_sync(~0u, f.b[v], off)
-                   : __shfl_up_sync(~0u, f.b[v], off);
-#pragma unroll
-    for (int v = 0; v < GV; ++v)
-      g.s[v] = REV ? __shfl_down_sync(~0u, f.s[v], off)
-                   : __shfl_up_sync(~0u, f.s[v], off);
-    const bool has = REV ? lane + off < 32 : lane >= off;
-    if (has) after<V, GV, GATE>(f, g);
-  }
-  if constexpr (L < 32) {
-    const bool first = REV ? lane + L >= 32 : lane < L;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float b = REV ? __shfl_down_sync(~0u, f.b[v], L)
-                          : __shfl_up_sync(~0u, f.b[v], L);
-      ex.b[v] = first ? 0.f : b;
-    }
-#pragma unroll
-    for (int v = 0; v < GV; ++v) {
-      const float s = REV ? __shfl_down_sync(~0u, f.s[v], L)
-                          : __shfl_up_sync(~0u, f.s[v], L);
-      ex.s[v] = first ? 0.f : s;
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) ex.b[v] = 0.f;
-#pragma unroll
-    for (int v = 0; v < GV; ++v) ex.s[v] = 0.f;
-  }
-}
-
-// The joins across the warps of a CTA and the CTAs of a cluster.  Thread
-// (warp w, lane) looks after channel `lane` of the tile: it leaves with the
-// value that enters warp w's tile, and `carry` moves on past all tiles of
-// this step.  One barrier per step: the buffers alternate.
-struct Joint {
-  float2 warp[2][kWarps][kCh];
-  float2 rank[2][kMaxCluster][kCh];
-};
-
-template <int GATE>
-__device__ __forceinline__ float apply(float2 m, float y) {
-  if constexpr (GATE == GDR_GATE_NONE) return y + m.y;
-  return decay(decay_factor(m.x), y) + m.y;
-}
-
-// `edge`: this thread belongs to the run that holds the whole warp's map
-// (the last in scan order).
-template <int V, int GV, int GATE, bool REV>
-__device__ __forceinline__ float block_join(Joint &jt, int buf,
-                                            const Map<V, GV> &f, bool edge,
-                                            int nc, int rank, float &carry) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = lane % (kCh / V);
-  if (edge) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      jt.warp[buf][w][c * V + v] =
-          make_float2(GATE == GDR_GATE_NONE ? 0.f : f.s[GV == V ? v : 0],
-                      f.b[v]);
-  }
-  __syncthreads();
-  float in = 0.f;
-  if (nc == 1) {
-    float y = carry;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const int j = REV ? kWarps - 1 - i : i;
-      if (j == w) in = y;
-      y = apply<GATE>(jt.warp[buf][j][lane], y);
-    }
-    carry = y;
-    return in;
-  }
-  float2 pre = make_float2(0.f, 0.f);   // the warps before this one
-  const int nbefore = REV ? kWarps - 1 - w : w;
-  for (int i = 0; i < nbefore; ++i) {
-    const float2 m = jt.warp[buf][REV ? kWarps - 1 - i : i][lane];
-    pre.y = apply<GATE>(m, pre.y);
-    pre.x += m.x;
-  }
-  if (nbefore == kWarps - 1) {
-    const float2 m = jt.warp[buf][w][lane];
-    const float2 tot = make_float2(pre.x + m.x, apply<GATE>(m, pre.y));
-    cg::cluster_group cl = cg::this_cluster();
-    for (int r = 0; r < nc; ++r)
-      cl.map_shared_rank(&jt.rank[buf][rank][lane], r)[0] = tot;
-  }
-  cg::this_cluster().sync();
-  float y = carry;
-  for (int r = 0; r < nc; ++r) {
-    if (r == rank) in = y;
-    y = apply<GATE>(jt.rank[buf][r][lane], y);
-  }
-  carry = y;
-  return apply<GATE>(pre, in);
-}
-
-// The same for a warp on its own: lane's channel of the warp's map.
-template <int V, int GV, int GATE, bool REV>
-__device__ __forceinline__ float warp_join(const Map<V, GV> &f,
-                                           float &carry) {
-  constexpr int L = kCh / V;
-  const int lane = threadIdx.x & 31;
-  const int src = (REV ? 0 : 32 - L) + lane / V;
-  float2 m = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const float b = __shfl_sync(~0u, f.b[v], src);
-    if (lane % V == v) m.y = b;
-  }
-  if constexpr (GATE != GDR_GATE_NONE) {
-#pragma unroll
-    for (int v = 0; v < GV; ++v) {
-      const float s = __shfl_sync(~0u, f.s[v], src);
-      if (GV == 1 || lane % V == v) m.x = s;
-    }
-  }
-  const float in = carry;
-  carry = apply<GATE>(m, carry);
-  return in;
-}
-
-// A thread's place: its chain (sequence and channel tile), its channels.
-struct Place {
-  int n;            // sequence
-  int ch;           // first of the thread's V channels
-  int chl;          // channel `lane` of the tile
-  bool has, hasl;   // whether those exist
-  int head, ct;     // the tile's head and tile within it (nct > 0)
-};
-template <int V>
-__device__ __forceinline__ Place place(const LinParams &p, int chain) {
-  Place q;
-  const int lane = threadIdx.x & 31;
-  const int tile = chain % p.tiles;
-  q.n = chain / p.tiles;
-  int base, end;
-  if (p.nct) {
-    q.head = tile / p.nct;
-    q.ct = tile - q.head * p.nct;
-    base = q.head * p.d + q.ct * kCh;
-    end = (q.head + 1) * p.d;
-  } else {
-    q.head = q.ct = 0;
-    base = tile * kCh;
-    end = p.D;
-  }
-  q.ch = base + (lane % (kCh / V)) * V;
-  q.chl = base + lane;
-  q.has = q.ch < end;
-  q.hasl = q.chl < end;
-  return q;
-}
-
 // ----------------------------------------------------------------- forward
 
-// WPC = 8: a cluster of CTAs per chain, stacked in time; WPC = 1: a warp per
-// chain.
-template <typename T, int V, int GATE, int WPC>
-__global__ void __launch_bounds__(kWarps * 32, 3)
+// WPC = kWarps: a chain (sequence and channel tile) by a CTA, or by a cluster
+// of them (CL), stacked in time; WPC = 1: by a warp.
+template <typename T, int LANES, bool VEC, int GATE, int WPC, bool CL>
+__global__ void __launch_bounds__(kWarps * 32, 4)
     gdr_linear_fwd_kernel(const LinParams p) {
-  using TL = Tile<V, GATE>;
-  constexpr int R = TL::R, GV = TL::GV, L = TL::kLanes;
-  using raw_t = typename Raw<T, V>::type;
-  __shared__ Joint jt;
+  using TL = Tile<LANES, GATE>;
+  constexpr int GV = TL::GV, CH = TL::kCh;
+  using IN = Inputs<T, VEC, GATE, false>;
+  using raw_t = typename IN::raw_t;
+  extern __shared__ __align__(128) char slots[];
+  __shared__ __align__(128) Joint<WPC == 1 ? 1 : CH, WPC> jt;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane / L;
+  const int sub = lane / LANES, c = lane % LANES;
   int nc = 1, rank = 0, chain;
   if constexpr (WPC == 1) {
     chain = blockIdx.x * kWarps + w;
     if (chain >= p.chains) return;
   } else {
-    nc = (int)cg::this_cluster().num_blocks();
-    rank = (int)cg::this_cluster().block_rank();
+    nc = p.nc;
+    if constexpr (CL) rank = (int)cg::this_cluster().block_rank();
     chain = blockIdx.x / nc;
-    // no CTA writes into another's shared memory before that one has begun
-    if (nc > 1) cg::this_cluster().sync();
+    if constexpr (CL) meet_first(jt);
   }
-  const Place q = place<V>(p, chain);
+  const Place q = place<LANES>(p, chain);
   int tok0, len;
   seq_range(p, q.n, &tok0, &len);
-  const long long so = (long long)q.n * p.D + q.chl;
-  float carry = (p.s0 && q.hasl) ? p.s0[so] : 0.f;
-  const int span = WPC == 1 ? kTok : kWarps * kTok * nc;
-  const int off = WPC == 1 ? 0 : (rank * kWarps + w) * kTok;
+  // the channel this thread carries the state of
+  const int own = WPC == 1 ? lane : threadIdx.x;
+  long long limit = p.wait_cycles;
+  const bool owns = own < CH && q.base + own < q.end;
+  const long long so = (long long)q.n * p.D + q.base + own;
+  float carry = (p.s0 && owns) ? p.s0[so] : 0.f;
+  constexpr int kBlock = WPC * TL::kTok;
+  const int span = kBlock * nc;
   const int steps = (len + span - 1) / span;
-  const int gcol = GATE == GDR_GATE_SCALAR ? q.ch / p.d : q.ch;
-  const int gld = GATE == GDR_GATE_SCALAR ? p.H : p.D;
+  // the thread's first token within the block's first step
+  const int t00 =
+      rank * kBlock + (WPC == 1 ? 0 : w * TL::kTok) + sub * kR;
+  IN in;
+  in.start(p, q, tok0, t00);
+  if (steps > 0) in.fetch(slots, t00, len);
+  T *op = static_cast<T *>(p.out) + ((long long)tok0 + t00) * p.D + q.ch;
+  float *sp =
+      p.states + ((long long)(tok0 / kR) + q.n + t00 / kR) * p.D + q.ch;
 
   for (int k = 0; k < steps; ++k) {
-    const int t0 = k * span + off;       // the warp's first token
-    const int t = t0 + sub * R;          // the thread's
-    const long long tok = (long long)tok0 + t;
-    raw_t xr[R];
-    float m[R][GV];
-    const T *xp = static_cast<const T *>(p.x) + tok * p.ldx + q.ch;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      xr[r] = raw_t{};
-      if (q.has && t + r < len)
-        xr[r] = __ldg(reinterpret_cast<const raw_t *>(xp + r * p.ldx));
-    }
-    if constexpr (GATE != GDR_GATE_NONE) {
-      const float *gp = p.la + tok * gld + gcol;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        typename Raw<float, GV>::type g{};
-        if (q.has && t + r < len)
-          g = __ldg(reinterpret_cast<const typename Raw<float, GV>::type *>(
-              gp + (long long)r * gld));
-        unpack(g, m[r]);
-      }
-    }
+    const int t = k * span + t00;                      // the thread's
+    raw_t xr[kR], dr[kR];
+    float m[kR][GV], none[kV];
+    in.move(span);
+    in.take(slots, xr, dr, m, none);
+    if (k + 1 < steps) in.fetch(slots, t + span, len);
     // the run on its own
-    Map<V, GV> f, ex;
+    Map<GV> f, ex;
 #pragma unroll
-    for (int v = 0; v < V; ++v) f.b[v] = 0.f;
+    for (int v = 0; v < kV; ++v) f.b[v] = 0.f;
 #pragma unroll
     for (int v = 0; v < GV; ++v) f.s[v] = 0.f;
+    const bool tight = is_tight<GV, GATE>(m);
+    auto alone = [&](auto tc) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float x[V];
-      unpack(xr[r], x);
-      if constexpr (GATE != GDR_GATE_NONE) {
-#pragma unroll
-        for (int v = 0; v < GV; ++v) {
-          f.s[v] += m[r][v];
-          m[r][v] = decay_factor(m[r][v]);
-        }
+      for (int r = 0; r < kR; ++r) {
+        float x[kV];
+        unpack(xr[r], x);
+        factors<GV, GATE, tc.value>(m[r], f.s);
+        advance<GV, GATE, tc.value>(f.b, m[r], x);
       }
+    };
+    if (tight) alone(Bool<true>{}); else alone(Bool<false>{});
+    const bool runs = is_tight_run<GV, GATE>(f.s, tight);
+    warp_scan<LANES, GV, GATE, false>(f, ex, runs);
+    // what enters the warp's tile
+    float h[kV];
+    if constexpr (WPC == 1) {
+      float2 mine = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        f.b[v] = (GATE == GDR_GATE_NONE
-                      ? f.b[v]
-                      : decay(m[r][GV == V ? v : 0], f.b[v])) + x[v];
+      for (int v = 0; v < kV; ++v) {
+        const int src = 32 - LANES + lane / kV;
+        const bool me = lane % kV == v;
+        const float b = __shfl_sync(~0u, f.b[v], src);
+        const float s = __shfl_sync(~0u, f.s[GV == kV ? v : 0], src);
+        if (me) mine = make_float2(s, b);
+        h[v] = __shfl_sync(~0u, carry, c * kV + v);
+      }
+      carry = apply<GATE>(mine, carry);
+    } else {
+      post<GV, GATE>(jt, f, c, sub == TL::kSubs - 1);
+      run_maps<CH, GATE, false, CL>(jt, k, nc, rank, limit, p.mute, carry);
+#pragma unroll
+      for (int v = 0; v < kV; ++v) h[v] = jt.in[w][c * kV + v];
     }
-    warp_scan<V, GV, GATE, false>(f, ex);
-    float hin;
-    if constexpr (WPC == 1)
-      hin = warp_join<V, GV, GATE, false>(f, carry);
-    else
-      hin = block_join<V, GV, GATE, false>(jt, k & 1, f, sub == TL::kSubs - 1,
-                                           nc, rank, carry);
-    if (p.states && q.hasl && t0 < len) {
-      const long long slot = (long long)(tok0 / kTok) + q.n + t0 / kTok;
-      p.states[slot * p.D + q.chl] = hin;
+    enter<LANES, GV, GATE>(h, ex, runs);
+    if (p.states) {
+      store<VEC>(sp, h, t < len ? q.nch : 0);
+      sp += (long long)(span / kR) * p.D;
     }
     if (p.out) {
-      float h[V];
+      auto again = [&](auto tc, auto full) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float y = __shfl_sync(~0u, hin, (lane % L) * V + v);
-        h[v] = apply<GATE>(make_float2(ex.s[GV == V ? v : 0], ex.b[v]), y);
-      }
-      T *op = static_cast<T *>(p.out) + tok * p.D + q.ch;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float x[V];
-        unpack(xr[r], x);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          h[v] = (GATE == GDR_GATE_NONE ? h[v]
-                                        : decay(m[r][GV == V ? v : 0], h[v])) +
-                 x[v];
-        if (q.has && t + r < len) store(op + (long long)r * p.D, h);
-      }
+        for (int r = 0; r < kR; ++r) {
+          float x[kV];
+          renew(xr[r]);
+          unpack(xr[r], x);
+          advance<GV, GATE, tc.value>(h, m[r], x);
+          if constexpr (VEC) {
+            if (full.value || (t + r < len && q.nch > 0))
+              store<true>(op + (long long)r * p.D, h, kV);
+          } else {
+            in.put(slots, r, h);
+          }
+        }
+      };
+      if (!tight)
+        again(Bool<false>{}, Bool<false>{});
+      else if (t + kR <= len && q.nch == kV)
+        again(Bool<true>{}, Bool<true>{});
+      else
+        again(Bool<true>{}, Bool<false>{});
+      if constexpr (!VEC) in.flush(slots);
+      op += (long long)span * p.D;
     }
   }
-  if (p.sT && q.hasl && (WPC == 1 || (rank == 0 && w == 0))) p.sT[so] = carry;
+  if (p.sT && owns && rank == 0) p.sT[so] = carry;
+  if constexpr (CL) cg::this_cluster().sync();
 }
 
 // ---------------------------------------------------------------- backward
 
-// From the last token to the first.  Every warp has its tile's first state
-// (the chunk states), so h is run forward inside the warp, leaving
-// alpha_t h_{t-1} in registers; then c runs backward through the same joins
-// as the forward pass.
-template <typename T, int V, int GATE, int WPC>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+// From the last token to the first.  Every thread runs h forward over its
+// tokens from their chunk state, leaving alpha_t h_{t-1} in registers; then c
+// runs backward through the same joins as the forward pass.
+template <typename T, int LANES, bool VEC, int GATE, int WPC, bool CL>
+__global__ void __launch_bounds__(kWarps * 32, 4)
     gdr_linear_bwd_kernel(const LinParams p) {
-  using TL = Tile<V, GATE>;
-  constexpr int R = TL::R, GV = TL::GV, L = TL::kLanes;
-  using raw_t = typename Raw<T, V>::type;
-  __shared__ Joint jt;
+  using TL = Tile<LANES, GATE>;
+  constexpr int GV = TL::GV, CH = TL::kCh;
+  using IN = Inputs<T, VEC, GATE, true>;
+  using raw_t = typename IN::raw_t;
+  extern __shared__ __align__(128) char slots[];
+  __shared__ __align__(128) Joint<WPC == 1 ? 1 : CH, WPC> jt;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane / L;
+  const int sub = lane / LANES, c = lane % LANES;
   int nc = 1, rank = 0, chain;
   if constexpr (WPC == 1) {
     chain = blockIdx.x * kWarps + w;
     if (chain >= p.chains) return;
   } else {
-    nc = (int)cg::this_cluster().num_blocks();
-    rank = (int)cg::this_cluster().block_rank();
+    nc = p.nc;
+    if constexpr (CL) rank = (int)cg::this_cluster().block_rank();
     chain = blockIdx.x / nc;
-    // no CTA writes into another's shared memory before that one has begun
-    if (nc > 1) cg::this_cluster().sync();
+    if constexpr (CL) meet_first(jt);
   }
-  const Place q = place<V>(p, chain);
+  const Place q = place<LANES>(p, chain);
   int tok0, len;
   seq_range(p, q.n, &tok0, &len);
-  const long long so = (long long)q.n * p.D + q.chl;
-  float carry = (p.dsT && q.hasl) ? p.dsT[so] : 0.f;
-  const int block = WPC == 1 ? kTok : kWarps * kTok;
-  const int nblk = (len + block - 1) / block;
+  const int own = WPC == 1 ? lane : threadIdx.x;
+  long long limit = p.wait_cycles;
+  const bool owns = own < CH && q.base + own < q.end;
+  const long long so = (long long)q.n * p.D + q.base + own;
+  float carry = (p.dsT && owns) ? p.dsT[so] : 0.f;
+  constexpr int kBlock = WPC * TL::kTok;
+  const int nblk = (len + kBlock - 1) / kBlock;
   const int steps = (nblk + nc - 1) / nc;
-  const int gcol = GATE == GDR_GATE_SCALAR ? q.ch / p.d : q.ch;
-  const int gld = GATE == GDR_GATE_SCALAR ? p.H : p.D;
+  // the first token of the block's and of the thread's step k; blocks before
+  // the first token hold none (end below all tokens)
+  auto block_at = [&](int k) { return (nblk - 1 - (k * nc + rank)) * kBlock; };
+  auto end_at = [&](int tb) { return tb < 0 ? INT_MIN : len; };
+  const int off = (WPC == 1 ? 0 : w * TL::kTok) + sub * kR;
+  IN in;
+  in.start(p, q, tok0, block_at(0) + off);
+  if (steps > 0) {
+    in.fetch(slots, block_at(0) + off, end_at(block_at(0)));
+    in.fetch_x(slots, in.x, block_at(0) + off, end_at(block_at(0)));
+  }
+  T *xo = static_cast<T *>(p.dx) +
+          ((long long)tok0 + block_at(0) + off) * p.D + q.ch;
 
   for (int k = 0; k < steps; ++k) {
-    const int blk = nblk - 1 - (k * nc + rank);
-    // (a block before the first token: nothing of it exists)
-    const int end = blk < 0 ? INT_MIN : len;
-    const int t0 = blk * block + (WPC == 1 ? 0 : w * kTok);
-    const int t = t0 + sub * R;
+    const int tb = block_at(k), end = end_at(tb);
+    const int t = tb + off;
     const long long tok = (long long)tok0 + t;
-    raw_t xr[R], dr[R];
-    float m[R][GV];
-    float h[V];
+    raw_t xr[kR], dr[kR];
+    float m[kR][GV], h[kV];
+    in.move(-kBlock * nc);
+    in.take(slots, xr, dr, m, h);
+    const int tn = block_at(k + 1);
+    if (k + 1 < steps) in.fetch(slots, tn + off, end_at(tn));
+    Map<GV> f, ex;
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = 0.f;
-    if constexpr (GATE != GDR_GATE_NONE) {
-      const T *xp = static_cast<const T *>(p.x) + tok * p.ldx + q.ch;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        xr[r] = raw_t{};
-        if (q.has && t + r < end)
-          xr[r] = __ldg(reinterpret_cast<const raw_t *>(xp + r * p.ldx));
-      }
-      const float *gp = p.la + tok * gld + gcol;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        typename Raw<float, GV>::type g{};
-        if (q.has && t + r < end)
-          g = __ldg(reinterpret_cast<const typename Raw<float, GV>::type *>(
-              gp + (long long)r * gld));
-        unpack(g, m[r]);
-      }
-      if (q.has && t0 < end) {
-        const long long slot = (long long)(tok0 / kTok) + q.n + t0 / kTok;
-        unpack(__ldg(reinterpret_cast<const typename Raw<float, V>::type *>(
-                   p.states + slot * p.D + q.ch)),
-               h);
-      }
-    }
-    const T *dp = static_cast<const T *>(p.dout) + tok * p.D + q.ch;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      dr[r] = raw_t{};
-      if (q.has && t + r < end)
-        dr[r] = __ldg(
-            reinterpret_cast<const raw_t *>(dp + (long long)r * p.D));
-    }
-    Map<V, GV> f, ex;
-#pragma unroll
-    for (int v = 0; v < V; ++v) f.b[v] = 0.f;
+    for (int v = 0; v < kV; ++v) f.b[v] = 0.f;
 #pragma unroll
     for (int v = 0; v < GV; ++v) f.s[v] = 0.f;
-    float ah[R][V];                      // alpha_t h_{t-1}
-    if constexpr (GATE != GDR_GATE_NONE) {
+    const bool tight = is_tight<GV, GATE>(m);
+    float ah[kR][kV];                    // alpha_t h_{t-1}
+    auto both = [&](auto tc) {
+      if constexpr (GATE != GDR_GATE_NONE) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float x[V];
-        unpack(xr[r], x);
+        for (int r = 0; r < kR; ++r) {
+          float x[kV];
+          unpack(in.x_at(slots, r), x);
+          factors<GV, GATE, tc.value>(m[r], f.s);
+          decay_all<GV, GATE, tc.value>(h, m[r]);
 #pragma unroll
-        for (int v = 0; v < GV; ++v) {
-          f.s[v] += m[r][v];
-          m[r][v] = decay_factor(m[r][v]);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          f.b[v] = decay(m[r][GV == V ? v : 0], f.b[v]) + x[v];
-      }
-      float ssum[GV];
-#pragma unroll
-      for (int v = 0; v < GV; ++v) ssum[v] = f.s[v];
-      warp_scan<V, GV, GATE, false>(f, ex);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        h[v] = apply<GATE>(make_float2(ex.s[GV == V ? v : 0], ex.b[v]), h[v]);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float x[V];
-        unpack(xr[r], x);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          ah[r][v] = decay(m[r][GV == V ? v : 0], h[v]);
-          h[v] = ah[r][v] + x[v];
+          for (int v = 0; v < kV; ++v) ah[r][v] = h[v];
+          add_all(h, x);
         }
       }
 #pragma unroll
-      for (int v = 0; v < GV; ++v) f.s[v] = ssum[v];
-#pragma unroll
-      for (int v = 0; v < V; ++v) f.b[v] = 0.f;
-    }
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-      float g[V];
-      unpack(dr[r], g);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        g[v] += f.b[v];
-        f.b[v] = GATE == GDR_GATE_NONE ? g[v]
-                                       : decay(m[r][GV == V ? v : 0], g[v]);
+      for (int r = kR - 1; r >= 0; --r) {
+        float g[kV];
+        unpack(dr[r], g);
+        add_all(f.b, g);
+        decay_all<GV, GATE, tc.value>(f.b, m[r]);
       }
-    }
-    warp_scan<V, GV, GATE, true>(f, ex);
-    float cin;
-    if constexpr (WPC == 1)
-      cin = warp_join<V, GV, GATE, true>(f, carry);
-    else
-      cin = block_join<V, GV, GATE, true>(jt, k & 1, f, sub == 0, nc, rank,
-                                          carry);
-    float c[V];
+    };
+    if (tight) both(Bool<true>{}); else both(Bool<false>{});
+    if (k + 1 < steps) in.fetch_x(slots, in.x, tn + off, end_at(tn));
+    const bool runs = is_tight_run<GV, GATE>(f.s, tight);
+    warp_scan<LANES, GV, GATE, true>(f, ex, runs);
+    float cy[kV];
+    if constexpr (WPC == 1) {
+      float2 mine = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float y = __shfl_sync(~0u, cin, (lane % L) * V + v);
-      c[v] = apply<GATE>(make_float2(ex.s[GV == V ? v : 0], ex.b[v]), y);
-    }
-    T *xo = static_cast<T *>(p.dx) + tok * p.D + q.ch;
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-      float g[V];
-      unpack(dr[r], g);
-#pragma unroll
-      for (int v = 0; v < V; ++v) g[v] += c[v];
-      const bool live = q.has && t + r < end;
-      if (live) store(xo + (long long)r * p.D, g);
-      if constexpr (GATE == GDR_GATE_CHANNEL) {
-        float dl[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) dl[v] = g[v] * ah[r][v];
-        if (live) store(p.dla + (tok + r) * p.D + q.ch, dl);
+      for (int v = 0; v < kV; ++v) {
+        const int src = lane / kV;
+        const bool me = lane % kV == v;
+        const float b = __shfl_sync(~0u, f.b[v], src);
+        const float s = __shfl_sync(~0u, f.s[GV == kV ? v : 0], src);
+        if (me) mine = make_float2(s, b);
+        cy[v] = __shfl_sync(~0u, carry, c * kV + v);
       }
-      if constexpr (GATE == GDR_GATE_SCALAR) {
-        // the head's share of this tile, added in a fixed order
-        float dl = 0.f;
+      carry = apply<GATE>(mine, carry);
+    } else {
+      post<GV, GATE>(jt, f, c, sub == 0);
+      run_maps<CH, GATE, true, CL>(jt, k, nc, rank, limit, p.mute, carry);
 #pragma unroll
-        for (int v = 0; v < V; ++v) dl = fmaf(g[v], ah[r][v], dl);
+      for (int v = 0; v < kV; ++v) cy[v] = jt.in[w][c * kV + v];
+    }
+    enter<LANES, GV, GATE>(cy, ex, runs);
+    auto again = [&](auto tc) {
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1)
-          dl += __shfl_xor_sync(~0u, dl, o);
-        if (live && lane % L == 0) {
-          if (p.nct == 1)
-            p.dla[(tok + r) * p.H + q.head] = dl;
+      for (int r = kR - 1; r >= 0; --r) {
+        float g[kV];
+        renew(dr[r]);
+        unpack(dr[r], g);
+        add_all(cy, g);
+        const int n = t + r < end ? q.nch : 0;
+        if constexpr (VEC)
+          store<true>(xo + (long long)r * p.D, cy, n);
+        else
+          in.put(slots, r, cy);
+        if constexpr (GATE == GDR_GATE_CHANNEL) {
+          float dl[kV];
+#pragma unroll
+          for (int v = 0; v < kV; ++v) dl[v] = cy[v] * ah[r][v];
+          if constexpr (VEC)
+            store<true>(p.dla + (tok + r) * p.D + q.ch, dl, n);
           else
-            p.part[((long long)q.ct * p.ntok + tok + r) * p.H + q.head] = dl;
+            in.put_la(slots, r, dl);
         }
-      }
+        if constexpr (GATE == GDR_GATE_SCALAR) {
+          // the head's share of this tile, added in a fixed order
+          float dl = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        c[v] = GATE == GDR_GATE_NONE ? g[v]
-                                     : decay(m[r][GV == V ? v : 0], g[v]);
-    }
+          for (int v = 0; v < kV; ++v) dl = fmaf(cy[v], ah[r][v], dl);
+#pragma unroll
+          for (int o = LANES / 2; o > 0; o >>= 1)
+            dl += __shfl_xor_sync(~0u, dl, o);
+          if (n && c == 0) {
+            if (p.nct == 1)
+              p.dla[(tok + r) * p.H + q.head] = dl;
+            else
+              p.part[((long long)q.ct * p.ntok + tok + r) * p.H + q.head] =
+                  dl;
+          }
+        }
+        decay_all<GV, GATE, tc.value>(cy, m[r]);
+      }
+    };
+    if (tight) again(Bool<true>{}); else again(Bool<false>{});
+    if constexpr (!VEC) in.flush(slots);
+    xo -= (long long)kBlock * nc * p.D;
   }
-  if (p.ds0 && q.hasl && (WPC == 1 || (rank == 0 && w == 0)))
-    p.ds0[so] = carry;
+  if (p.ds0 && owns && rank == 0) p.ds0[so] = carry;
+  if constexpr (CL) cg::this_cluster().sync();
 }
 
 // Scalar gate, heads of more than one channel tile: the tiles' shares of
@@ -660,128 +1223,183 @@ __global__ void __launch_bounds__(256)
 
 // -------------------------------------------------------------------- step
 
-template <typename T, int V, int GATE>
+__device__ __forceinline__ float to_float(float f) { return f; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 f) {
+  return __bfloat162float(f);
+}
+
+// A thread has four channels (VEC) or one.
+template <typename T, bool VEC, int GATE>
 __global__ void __launch_bounds__(128)
     gdr_linear_step_kernel(const T *x, const float *la, const float *sin,
                            float *sout, T *out, long long ldx, int N, int H,
                            int d) {
+  constexpr int V = VEC ? kV : 1;
   const int D = H * d, nv = D / V;
   const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
   if (i >= (long long)N * nv) return;
   const long long n = i / nv;
   const int ch = (int)(i - n * nv) * V;
-  float xf[V], h[V];
-  using raw_t = typename Raw<T, V>::type;
-  using f_t = typename Raw<float, V>::type;
-  unpack(__ldg(reinterpret_cast<const raw_t *>(x + n * ldx + ch)), xf);
+  float xf[kV], h[kV] = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (VEC)
+    unpack(__ldg(reinterpret_cast<const typename Raw<T>::type *>(
+               x + n * ldx + ch)),
+           xf);
+  else
+    xf[0] = to_float(x[n * ldx + ch]);
+  if (sin) {   // (may be sout: not through the read-only path)
+    const float *sp = sin + n * D + ch;
+    if constexpr (VEC)
+      unpack(*reinterpret_cast<const float4 *>(sp), h);
+    else
+      h[0] = *sp;
+  }
+  if constexpr (GATE != GDR_GATE_NONE) {
+    float g[kV];
+    if constexpr (GATE == GDR_GATE_CHANNEL) {
+      if constexpr (VEC)
+        unpack(__ldg(reinterpret_cast<const float4 *>(la + n * D + ch)), g);
+      else
+        g[0] = __ldg(la + n * D + ch);
+    } else {
+      g[0] = __ldg(la + n * H + ch / d);
+    }
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = 0.f;
-  if (sin) unpack(*reinterpret_cast<const f_t *>(sin + n * D + ch), h);
-  if constexpr (GATE == GDR_GATE_CHANNEL) {
-    float g[V];
-    unpack(__ldg(reinterpret_cast<const f_t *>(la + n * D + ch)), g);
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = decay(decay_factor(g[v]), h[v]);
-  } else if constexpr (GATE == GDR_GATE_SCALAR) {
-    const float m = decay_factor(__ldg(la + n * H + ch / d));
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = decay(m, h[v]);
+    for (int v = 0; v < V; ++v)
+      h[v] = decay<false>(
+          decay_factor<false>(g[GATE == GDR_GATE_CHANNEL ? v : 0]), h[v]);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] += xf[v];
-  store(out + n * D + ch, h);
-  store(sout + n * D + ch, h);
+  store<VEC>(out + n * D + ch, h, 1);
+  store<VEC>(sout + n * D + ch, h, 1);
 }
 
 // ---------------------------------------------------------------- launches
 
-// A chain is run by a warp where there are chains enough to fill the GPU so
-// (or the sequences are too short to cut), else by a cluster of CTAs.
+enum Op { kFwd, kBwd, kStep };
+
+// How a call is cut.
+struct Plan {
+  bool vec;        // rows are aligned for vectors of four channels
+  int lanes, wpc;  // a warp's tile is 4 lanes channels wide; warps per chain
+  int nc;          // CTAs per chain
+};
+
 constexpr int kSms = 148;
-
-int cluster_size(const LinParams &p, int resident) {
-  const long long avg = p.ntok / (p.nseq > 0 ? p.nseq : 1);
-  const long long blocks = (avg + kWarps * kTok - 1) / (kWarps * kTok);
-  int nc = 1;
-  while (nc * 2 <= kMaxCluster && nc * 2 <= blocks &&
-         (long long)p.chains * nc * 2 <= (long long)kSms * resident)
-    nc *= 2;
-  return nc;
-}
-
-bool warp_chains(const LinParams &p) {
-  const long long avg = p.ntok / (p.nseq > 0 ? p.nseq : 1);
-  return avg <= 2 * kTok || p.chains >= kSms * 3 * kWarps;
+gdr_status plan(Op op, const gdr_opts &o, LinParams *p, Plan *pl) {
+  const bool bf16 = o.dtype == GDR_BF16, bwd = op == kBwd;
+  // one vector must not span two decays
+  pl->vec = p->D % kV == 0 && p->ldx % kV == 0 &&
+            (o.gate != GDR_GATE_SCALAR || p->d % kV == 0);
+  // 64 channels by 16 tokens in the backward pass of bf16, whose tiles then
+  // take one shuffle round fewer; of fp32 they would leave room for fewer
+  // CTAs, and the forward pass is as fast either way but makes twice the
+  // chains
+  const int wide = bwd && bf16 && pl->vec ? 16 : 8;
+  const int btok = kWarps * kR * 32 / wide;
+  const int avg = p->ntok / p->nseq;
+  auto cut = [&](int lanes) {
+    pl->lanes = lanes;
+    const int ch = kV * lanes;
+    // a scalar decay's gradient is summed per head, so its tiles keep to one;
+    // so do those of rows that are not aligned
+    const bool per_head = o.gate == GDR_GATE_SCALAR && (bwd || !pl->vec);
+    p->nct = per_head ? (p->d + ch - 1) / ch : 0;
+    p->tiles = per_head ? p->H * p->nct : (p->D + ch - 1) / ch;
+    return (long long)p->tiles * p->nseq;
+  };
+  // Sequences too short for a CTA's tile are run by single warps.  So are, in
+  // the forward pass, those up to half as long again, if they alone fill the
+  // GPU (bf16, 2048 channels, 33.5 M tokens x channels: 96 tokens 97 us
+  // against 136, 192 tokens 100 against 124, 256 tokens 101 against 92).
+  long long chains = cut(8);
+  const bool short_seqs =
+      2 * avg <= btok || (!bwd && pl->vec && 2 * avg <= 3 * btok &&
+                          chains >= 4ll * kSms * kWarps);
+  pl->wpc = short_seqs ? 1 : kWarps;
+  if (!short_seqs) chains = cut(wide);
+  if (chains > INT_MAX / kMaxCluster) return GDR_ERR_UNSUPPORTED;
+  p->chains = (int)chains;
+  // CTAs per chain: the more, the more of a long sequence is under way at
+  // once, but a step then waits for all of them.  Best as long as the launch
+  // stays about this big (forward, bf16, 512 chains of 4096 tokens: 1 CTA
+  // 93 us, 8 CTAs 126; 64 chains of 65536: 1 CTA 720 us, 8 CTAs 228;
+  // backward, 256 chains of 4096: 1 CTA 167, 2 205, 8 169).
+  const int ctas = bwd ? (bf16 ? 2048 : 1024) : bf16 ? 4 * kSms : 2048;
+  pl->nc = 1;
+  if (pl->wpc > 1)
+    while (pl->nc < kMaxCluster && pl->nc * btok < avg &&
+           chains * pl->nc * 2 <= ctas)
+      pl->nc *= 2;
+  return GDR_OK;
 }
 
 template <typename K>
-cudaError_t launch_chains(K kernel, const LinParams &p, int wpc, int nc,
-                          cudaStream_t s) {
+cudaError_t launch_chains(K kernel, int slots, const LinParams &p,
+                          const Plan &pl, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, slots);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(wpc == 1 ? (p.chains + kWarps - 1) / kWarps
-                              : p.chains * nc);
+  cfg.gridDim = dim3(pl.wpc == 1 ? (p.chains + kWarps - 1) / kWarps
+                                 : p.chains * pl.nc);
+  LinParams q = p;
+  q.nc = pl.nc;
   cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = slots;
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = wpc == 1 ? 1 : nc;
+  at.val.clusterDim.x = pl.nc;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  cfg.numAttrs = pl.nc > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, q);
 }
 
-template <typename T, int V, int GATE>
-cudaError_t run_fwd(const LinParams &p, cudaStream_t s) {
-  if (warp_chains(p))
-    return launch_chains(gdr_linear_fwd_kernel<T, V, GATE, 1>, p, 1, 1, s);
-  return launch_chains(gdr_linear_fwd_kernel<T, V, GATE, kWarps>, p, kWarps,
-                       cluster_size(p, 3), s);
+template <typename T, bool VEC, int GATE, bool WARP, bool CL>
+cudaError_t run4(Op op, const LinParams &p, const Plan &pl, cudaStream_t s) {
+  constexpr int kWpc = WARP ? 1 : kWarps;
+  constexpr int kWide = !WARP && VEC && sizeof(T) == 2 ? 16 : 8;   // as plan()
+  return op == kFwd
+             ? launch_chains(gdr_linear_fwd_kernel<T, 8, VEC, GATE, kWpc, CL>,
+                             Inputs<T, VEC, GATE, false>::kBytes, p, pl, s)
+             : launch_chains(
+                   gdr_linear_bwd_kernel<T, kWide, VEC, GATE, kWpc, CL>,
+                   Inputs<T, VEC, GATE, true>::kBytes, p, pl, s);
 }
-template <typename T, int V, int GATE>
-cudaError_t run_bwd(const LinParams &p, cudaStream_t s) {
-  if (warp_chains(p))
-    return launch_chains(gdr_linear_bwd_kernel<T, V, GATE, 1>, p, 1, 1, s);
-  return launch_chains(gdr_linear_bwd_kernel<T, V, GATE, kWarps>, p, kWarps,
-                       cluster_size(p, 2), s);
+template <typename T, bool VEC, int GATE>
+cudaError_t run3(Op op, const LinParams &p, const Plan &pl, cudaStream_t s) {
+  if (op == kStep) {
+    const long long n = (long long)p.nseq * (p.D / (VEC ? kV : 1));
+    gdr_linear_step_kernel<T, VEC, GATE>
+        <<<(unsigned)((n + 127) / 128), 128, 0, s>>>(
+            static_cast<const T *>(p.x), p.la, p.s0, p.sT,
+            static_cast<T *>(p.out), p.ldx, p.nseq, p.H, p.d);
+    return cudaGetLastError();
+  }
+  return pl.wpc == 1  ? run4<T, VEC, GATE, true, false>(op, p, pl, s)
+         : pl.nc == 1 ? run4<T, VEC, GATE, false, false>(op, p, pl, s)
+                      : run4<T, VEC, GATE, false, true>(op, p, pl, s);
 }
-template <typename T, int V, int GATE>
-cudaError_t run_step(const LinParams &p, cudaStream_t s) {
-  const long long n = (long long)p.nseq * (p.D / V);
-  gdr_linear_step_kernel<T, V, GATE><<<(unsigned)((n + 127) / 128), 128, 0,
-                                       s>>>(
-      static_cast<const T *>(p.x), p.la, p.s0, p.sT,
-      static_cast<T *>(p.out), p.ldx, p.nseq, p.H, p.d);
-  return cudaGetLastError();
-}
-
-enum Op { kFwd, kBwd, kStep };
-
-template <typename T, int V, int GATE>
-cudaError_t run3(Op op, const LinParams &p, cudaStream_t s) {
-  return op == kFwd ? run_fwd<T, V, GATE>(p, s)
-                    : op == kBwd ? run_bwd<T, V, GATE>(p, s)
-                                 : run_step<T, V, GATE>(p, s);
-}
-template <typename T, int V>
-cudaError_t run2(Op op, int gate, const LinParams &p, cudaStream_t s) {
+template <typename T, bool VEC>
+cudaError_t run2(Op op, int gate, const LinParams &p, const Plan &pl,
+                 cudaStream_t s) {
   switch (gate) {
-    case GDR_GATE_NONE: return run3<T, V, GDR_GATE_NONE>(op, p, s);
-    case GDR_GATE_SCALAR: return run3<T, V, GDR_GATE_SCALAR>(op, p, s);
-    default: return run3<T, V, GDR_GATE_CHANNEL>(op, p, s);
+    case GDR_GATE_NONE: return run3<T, VEC, GDR_GATE_NONE>(op, p, pl, s);
+    case GDR_GATE_SCALAR: return run3<T, VEC, GDR_GATE_SCALAR>(op, p, pl, s);
+    default: return run3<T, VEC, GDR_GATE_CHANNEL>(op, p, pl, s);
   }
 }
-// Four channels a thread where rows keep 16-byte (fp32) alignment and a
-// vector stays within a head; else one.
-cudaError_t run(Op op, const gdr_opts &o, const LinParams &p, cudaStream_t s) {
-  const bool v4 = p.D % 4 == 0 && p.ldx % 4 == 0 &&
-                  (o.gate != GDR_GATE_SCALAR || p.d % 4 == 0);
+cudaError_t run(Op op, const gdr_opts &o, const LinParams &p, const Plan &pl,
+                cudaStream_t s) {
   if (o.dtype == GDR_BF16)
-    return v4 ? run2<__nv_bfloat16, 4>(op, o.gate, p, s)
-              : run2<__nv_bfloat16, 1>(op, o.gate, p, s);
-  return v4 ? run2<float, 4>(op, o.gate, p, s)
-            : run2<float, 1>(op, o.gate, p, s);
+    return pl.vec ? run2<__nv_bfloat16, true>(op, o.gate, p, pl, s)
+                  : run2<__nv_bfloat16, false>(op, o.gate, p, pl, s);
+  return pl.vec ? run2<float, true>(op, o.gate, p, pl, s)
+                : run2<float, false>(op, o.gate, p, pl, s);
 }
 
 // ------------------------------------------------------------------ checks
@@ -841,7 +1459,11 @@ gdr_status check_common(const gdr_opts *opts, gdr_opts *o, LinParams *p,
   const long long ntok = packed ? T : (long long)B * T;
   if (ntok > INT_MAX / 2) return GDR_ERR_UNSUPPORTED;
   if (ldx < D) return GDR_ERR_INVALID_ARGUMENT;
+  if (ldx > INT_MAX / 2) return GDR_ERR_UNSUPPORTED;
   std::memset(p, 0, sizeof(*p));
+  const char *inj = std::getenv("GDR_FAULT_INJECT_LINEAR_TIMEOUT");
+  p->mute = inj && inj[0] == '1';
+  p->wait_cycles = p->mute ? kInjectWaitCycles : kWaitCycles;
   p->nseq = packed ? o->num_seqs : B;
   p->T = T;
   p->ntok = (int)ntok;
@@ -858,17 +1480,18 @@ gdr_status check_common(const gdr_opts *opts, gdr_opts *o, LinParams *p,
   return GDR_OK;
 }
 
-// Cuts the channels into tiles; the chains have to fit the launch grid.
-gdr_status cut(LinParams *p, bool per_head) {
-  p->nct = per_head ? (p->d + kCh - 1) / kCh : 0;
-  p->tiles = per_head ? p->H * p->nct : (p->D + kCh - 1) / kCh;
-  const long long chains = (long long)p->tiles * p->nseq;
-  if (chains > INT_MAX / kMaxCluster) return GDR_ERR_UNSUPPORTED;
-  p->chains = (int)chains;
-  return GDR_OK;
+}  // namespace
+
+cudaError_t linear_read_error(unsigned *word, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_linear_error, sizeof(unsigned));
+  if (e != cudaSuccess) return e;
+  if (clear && *word) {
+    const unsigned zero = 0;
+    e = cudaMemcpyToSymbol(g_linear_error, &zero, sizeof(unsigned));
+  }
+  return e;
 }
 
-}  // namespace
 }  // namespace gdr
 
 extern "C" gdr_status gdr_linear_fwd(const void *x, long long ldx,
@@ -907,9 +1530,10 @@ extern "C" gdr_status gdr_linear_fwd(const void *x, long long ldx,
   p.out = out;
   p.sT = final_state;
   p.states = chunk_states;
-  st = cut(&p, false);
+  Plan pl;
+  st = plan(kFwd, o, &p, &pl);
   if (st != GDR_OK) return st;
-  return run(kFwd, o, p, stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+  return run(kFwd, o, p, pl, stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
 extern "C" gdr_status gdr_linear_step(const void *x, long long ldx,
@@ -943,7 +1567,10 @@ extern "C" gdr_status gdr_linear_step(const void *x, long long ldx,
   p.s0 = state_in;
   p.sT = state_out;
   p.out = out;
-  return run(kStep, o, p, stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+  Plan pl;
+  st = plan(kStep, o, &p, &pl);
+  if (st != GDR_OK) return st;
+  return run(kStep, o, p, pl, stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
 extern "C" gdr_status gdr_linear_backward(
@@ -986,8 +1613,9 @@ extern "C" gdr_status gdr_linear_backward(
   if (overlaps(wr, 3, rd, 6)) return GDR_ERR_INVALID_ARGUMENT;
   const bool scalar = o.gate == GDR_GATE_SCALAR;
   LinParams pf = p;
-  st = cut(&pf, false);
-  if (st == GDR_OK) st = cut(&p, scalar);
+  Plan plf, pl;
+  st = plan(kFwd, o, &pf, &plf);
+  if (st == GDR_OK) st = plan(kBwd, o, &p, &pl);
   if (st != GDR_OK) return st;
   // scratch: the chunk states where the caller has none (no gate needs
   // none), the channel tiles' shares of dlog_alpha
@@ -1006,7 +1634,7 @@ extern "C" gdr_status gdr_linear_backward(
     p.states = static_cast<float *>(ws);
     pf.s0 = initial_state;
     pf.states = p.states;
-    e = run(kFwd, o, pf, stream);
+    e = run(kFwd, o, pf, plf, stream);
   }
   p.dout = d_out;
   p.dsT = d_final_state;
@@ -1014,7 +1642,7 @@ extern "C" gdr_status gdr_linear_backward(
   p.dla = d_log_alpha;
   p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + sbytes);
   p.ds0 = d_initial_state;
-  if (e == cudaSuccess) e = run(kBwd, o, p, stream);
+  if (e == cudaSuccess) e = run(kBwd, o, p, pl, stream);
   if (e == cudaSuccess && parts && p.ntok > 0) {
     const long long nh = (long long)p.ntok * H;
     gdr_linear_dla_kernel<<<(unsigned)((nh + 255) / 256), 256, 0, stream>>>(

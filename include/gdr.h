@@ -609,11 +609,11 @@ GDR_API gdr_status gdr_efla_beta_backward(const void *k, const float *beta,
  *   final_state   [N][H][d] fp32 (written), or NULL to skip; a sequence of no
  *                 tokens ends in its initial state
  *   chunk_states  [T_all / GDR_LINEAR_CHUNK + N][H][d] fp32 (written), or
- *                 NULL to skip: the state in front of every 32nd token of
+ *                 NULL to skip: the state in front of every 8th token of
  *                 every sequence, for gdr_linear_backward, which else has to
  *                 compute them again.  T_all is B * T, or T with cu_seqlens;
  *                 sequence n, whose first token is a, has the entries from
- *                 a / 32 + n on; entries between are not written.
+ *                 a / 8 + n on; entries between are not written.
  * where N = B, or num_seqs with cu_seqlens (then B = 1).  Offsets have to be
  * non-decreasing within [0, T]; rows of out outside every sequence are left
  * as they were.  Buffers that are written must not overlap any other.
@@ -623,7 +623,7 @@ GDR_API gdr_status gdr_efla_beta_backward(const void *k, const float *beta,
  * once.  opts->algo must be AUTO.  One launch, no scratch; results do not
  * depend on scheduling.
  */
-#define GDR_LINEAR_CHUNK 32
+#define GDR_LINEAR_CHUNK 8
 
 GDR_API gdr_status gdr_linear_fwd(const void *x, long long ldx,
                                   const float *log_alpha,

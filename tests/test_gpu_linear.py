@@ -112,7 +112,7 @@ def check_bwd(x, la, s0, dO, dS, res, cu=None):
 SHAPES = [(1, 1, 1, 16), (2, 7, 3, 33), (1, 31, 2, 100), (3, 32, 1, 4),
           (2, 33, 5, 1), (1, 64, 16, 128), (2, 65, 2, 72), (1, 255, 2, 36),
           (1, 256, 1, 64), (2, 257, 4, 20), (1, 1000, 3, 50),
-          (1, 2600, 2, 48)]
+          (1, 2600, 2, 48), (1, 1500, 1, 37), (3, 300, 5, 13)]
 
 
 @pytest.mark.parametrize("gate", ["none", "scalar", "channel"])
@@ -241,6 +241,24 @@ def test_strided_tokens(gate):
         sb = gdr.linear_step(xs[:, 0], None if la is None else
                              la[:, 0].contiguous(), s0, state_out=s0.clone())
         assert torch.equal(sa[0], sb[0]) and torch.equal(sa[1], sb[1])
+
+
+@pytest.mark.parametrize("gate", ["none", "scalar", "channel"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 41, 1, 37), (2, 300, 3, 20),
+                                   (1, 700, 1, 5)])
+def test_nothing_is_written_beside_the_results(shape, dtype, gate):
+    x, la, s0, dO, dS = inputs(*shape, dtype, gate)
+    n = x.numel()
+    wide = torch.full((n + 64,), 7.0, dtype=x.dtype, device="cuda")
+    fin = torch.full((s0.numel() + 64,), 7.0, device="cuda")
+    gdr.linear_fwd(x, la, s0, out=wide[32:32 + n].view(x.shape),
+                   final_state=fin[32:32 + s0.numel()].view(s0.shape))
+    torch.cuda.synchronize()
+    check_fwd(x, la, s0, wide[32:32 + n].view(x.shape),
+              fin[32:32 + s0.numel()].view(s0.shape))
+    for t, m in ((wide, n), (fin, s0.numel())):
+        assert (t[:32] == 7).all() and (t[32 + m:] == 7).all()
 
 
 @pytest.mark.parametrize("gate", ["none", "scalar", "channel"])
@@ -390,3 +408,16 @@ def test_binding_refuses_what_the_kernels_cannot_take():
     with pytest.raises(gdr.GdrError):          # base off by two bytes
         wide = torch.zeros(2, 8, 40, device="cuda", dtype=torch.bfloat16)
         gdr.linear_fwd(wide[..., 1:33].unflatten(-1, (2, 16)), la)
+
+
+def test_an_expired_wait_is_reported(monkeypatch):
+    """CTAs of a cluster that never hear from one another give up, the call
+    ends and says so, and the next one is right."""
+    x, la, s0, dO, dS = inputs(1, 2000, 1, 64, "fp32", "channel")
+    monkeypatch.setenv("GDR_FAULT_INJECT_LINEAR_TIMEOUT", "1")
+    gdr.linear_fwd(x, la, s0)
+    assert gdr.STATUS[gdr.device_error()] == "GDR_ERR_TIMEOUT"
+    monkeypatch.delenv("GDR_FAULT_INJECT_LINEAR_TIMEOUT")
+    out, fin = gdr.linear_fwd(x, la, s0)
+    assert gdr.device_error() == 0
+    check_fwd(x, la, s0, out, fin)
