@@ -670,6 +670,11 @@ def _launch(x, stream, call):
         return call(stream.cuda_stream)
 
 
+def _like(x):
+    """A contiguous tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 _plain_opts = {}
 
 
@@ -739,7 +744,7 @@ def linear_fwd(x, log_alpha=None, initial_state=None, *,
     _check("final_state", final_state, (nseq, H, d), torch.float32, x)
 
     def call(handle):
-        o = out if out is not None else x.new_empty(x.shape)
+        o = out if out is not None else _like(x)
         fin = final_state
         if fin is None and output_final_state:
             fin = x.new_empty((nseq, H, d), dtype=torch.float32)
@@ -781,7 +786,7 @@ def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
     opts = _opts_of(x, g)
 
     def call(handle):
-        o = out if out is not None else x.new_empty(shape)
+        o = out if out is not None else _like(x)
         so = state_out if state_out is not None else state
         if so is None:
             so = x.new_empty(shape, dtype=torch.float32)
@@ -817,9 +822,8 @@ def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
                 (B * T // LINEAR_CHUNK + nseq, H, d), torch.float32, x)
 
     def call(handle):
-        dx = x.new_empty(x.shape)
-        gla = None if log_alpha is None else log_alpha.new_empty(
-            log_alpha.shape)
+        dx = _like(x)
+        gla = None if log_alpha is None else torch.empty_like(log_alpha)
         gs0 = (x.new_empty((nseq, H, d), dtype=torch.float32)
                if need_initial_state_grad else None)
         rc = lib.gdr_linear_backward(
@@ -866,7 +870,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
     _check("out", out, x.shape, x.dtype, x)
 
     def call(handle):
-        o = out if out is not None else x.new_empty(x.shape)
+        o = out if out is not None else _like(x)
         rc = lib.gdr_layer_norm(x.data_ptr(), ldx, w, b, o.data_ptr(), ntok,
                                 H, d, eps, DTYPES[x.dtype], handle)
         if rc != 0:
@@ -889,10 +893,10 @@ def layer_norm_backward(x, weight, d_out, *, eps: float = 1e-5,
         raise ValueError("d_out must be given")
 
     def call(handle):
-        dx = x.new_empty(x.shape)
+        dx = _like(x)
         dw = db = None
         if need_param_grads and weight is not None:
-            dw, db = weight.new_empty(shape), weight.new_empty(shape)
+            dw, db = torch.empty_like(weight), torch.empty_like(weight)
         rc = lib.gdr_layer_norm_backward(
             x.data_ptr(), ldx, w, dy, dx.data_ptr(),
             None if dw is None else dw.data_ptr(),

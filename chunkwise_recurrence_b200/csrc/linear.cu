@@ -32,6 +32,7 @@
 
 #include "gdr_internal.h"
 #include "sm100.cuh"
+#include "streaming.cuh"
 
 namespace gdr {
 
@@ -41,6 +42,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 using namespace sm100;
+using namespace streaming;
 
 constexpr int kV = 4;            // channels of a thread
 constexpr int kR = 8;            // tokens of a thread's run
@@ -92,10 +94,6 @@ __device__ __forceinline__ void unpack(const uint2 &r, float (&f)[kV]) {
   f[0] = __uint_as_float(r.x << 16), f[1] = __uint_as_float(r.x & 0xffff0000u);
   f[2] = __uint_as_float(r.y << 16), f[3] = __uint_as_float(r.y & 0xffff0000u);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&p);
-}
 // Forgets what the compiler knows about a loaded value, so that it does not
 // keep the unpacked elements in registers from one pass to the next.
 __device__ __forceinline__ void renew(uint2 &r) {
@@ -128,55 +126,6 @@ __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[kV],
     for (int v = 0; v < kV; ++v)
       if (n > v) p[v] = __float2bfloat16_rn(f[v]);
   }
-}
-
-// Asynchronous copy of `bytes` <= N bytes (N = 4, 8 or 16) into N bytes of
-// shared memory; the rest is zero and not read.
-template <int N>
-__device__ __forceinline__ void copy_async(void *dst, const void *src,
-                                           int bytes) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
-                 "l"(src), "r"(bytes)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d),
-                 "l"(src), "n"(N), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_landed() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-// Two fp32 values in a register pair, for the instructions that work on both
-// at once.
-struct Pair {
-  unsigned long long u;
-};
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-  Pair p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p.u) : "f"(lo), "f"(hi));
-  return p;
-}
-__device__ __forceinline__ void split(Pair p, float &lo, float &hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p.u));
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(d.u) : "l"(a.u), "l"(b.u), "l"(c.u));
-  return d;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(a.u), "l"(b.u));
-  return d;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-  Pair d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(a.u), "l"(b.u));
-  return d;
 }
 
 // ------------------------------------------------------------------ decays

@@ -98,7 +98,8 @@ SHAPES = [(1, 1, 1), (3, 1, 2), (5, 2, 8), (7, 3, 9), (4, 5, 16), (9, 1, 31),
           (33, 16, 128), (6, 7, 64), (2, 3, 100), (65, 1, 257), (17, 2, 300),
           (40, 1, 1001), (21, 1, 2048), (9, 2, 2056), (300, 1, 512),
           (5, 1, 4097), (6, 1, 5120), (3, 1, 8192), (2, 1, 12000),
-          (3, 1, 16383), (2, 1, 16384), (700, 33, 24)]
+          (3, 1, 16383), (2, 1, 16384), (700, 33, 24), (10000, 1, 77),
+          (4000, 5, 101), (3001, 1, 1001), (1300, 1, 2047), (900, 1, 4101)]
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
@@ -136,6 +137,18 @@ def test_large_offsets_keep_the_variance():
     x = x + 1000.0
     check_fwd(x, w, b, gdr.layer_norm(x, w, b))
     check_bwd(x, w, dy, gdr.layer_norm_backward(x, w, dy))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(37, 1, 13), (5, 3, 7), (300, 1, 1001),
+                                   (3, 2, 64)])
+def test_nothing_is_written_beside_the_result(shape, dtype):
+    x, w, b, _ = inputs(*shape, dtype)
+    n = x.numel()
+    wide = torch.full((n + 64,), 7.0, dtype=x.dtype, device="cuda")
+    y = gdr.layer_norm(x, w, b, out=wide[32:32 + n].view(x.shape))
+    check_fwd(x, w, b, y)
+    assert (wide[:32] == 7).all() and (wide[32 + n:] == 7).all()
 
 
 def test_constant_rows_give_the_bias():
