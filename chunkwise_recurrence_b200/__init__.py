@@ -595,27 +595,28 @@ def efla_beta_backward(k, beta, d_beta_prime, dk, *, d_beta=None,
 # Linear recurrence and layer normalisation.  Unlike the entries above, these
 # check every tensor (ValueError) before they call the library.
 
-def _activation(name, x, inner):
+def _activation(x, inner):
     """Checks a device tensor of activations [.., inner dims] whose inner
-    dimensions are contiguous and whose tokens are evenly spaced; returns the
-    distance between tokens in elements."""
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if x.dtype not in DTYPES:
-        raise ValueError(f"{name} must be bfloat16 or float32")
+    dimensions are contiguous and whose tokens are evenly spaced; returns
+    (shape, distance between tokens in elements, device)."""
     shape = x.shape
     outer = len(shape) - inner
-    step = 1
+    if outer < 0:
+        raise ValueError(f"x must have at least {inner} dimension(s)")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dtype not in DTYPES:
+        raise ValueError("x must be bfloat16 or float32")
+    step = shape[-1] if inner == 1 else shape[-1] * shape[-2]
     if x.is_contiguous():
-        for n in shape[outer:]:
-            step *= n
-        return step
+        return shape, step, x.get_device()
     strides = x.stride()
+    n = 1
     for i in range(len(shape) - 1, outer - 1, -1):
-        if shape[i] != 1 and strides[i] != step:
-            raise ValueError(f"{name}: the last {inner} dimension(s) must be "
+        if shape[i] != 1 and strides[i] != n:
+            raise ValueError(f"x: the last {inner} dimension(s) must be "
                              "contiguous")
-        step *= shape[i]
+        n *= shape[i]
     ld, rows = None, 1
     for i in range(outer - 1, -1, -1):
         if shape[i] == 1:
@@ -623,28 +624,28 @@ def _activation(name, x, inner):
         if ld is None:
             ld = strides[i]
             if ld < step:
-                raise ValueError(f"{name}: tokens must not overlap")
+                raise ValueError("x: tokens must not overlap")
         elif strides[i] != ld * rows:
-            raise ValueError(f"{name}: tokens must be evenly spaced")
+            raise ValueError("x: tokens must be evenly spaced")
         rows *= shape[i]
-    return step if ld is None else ld
+    return shape, step if ld is None else ld, x.get_device()
 
 
-def _check(name, t, shape, dtype, x):
-    """Checks another tensor of the call whose activations are x; returns its
-    address (None for None)."""
+def _check(name, t, shape, dtype, device):
+    """Checks another tensor of a call whose activations are on `device`;
+    returns its address (None for None)."""
     if t is None:
         return None
     if (t.shape == shape and t.dtype is dtype and t.is_contiguous() and
-            t.get_device() == x.get_device()):
+            t.get_device() == device):
         return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, "
                          f"not {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != x.device:
-        raise ValueError(f"{name} must be on {x.device}, not {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, not {t.device}")
     raise ValueError(f"{name} must be contiguous")
 
 
@@ -653,19 +654,19 @@ def _check(name, t, shape, dtype, x):
 _raw_stream = getattr(
     torch._C, "_cuda_getCurrentRawStream",
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = torch.cuda.current_device
 
 
-def _launch(x, stream, call):
-    """call(stream handle) with x's device and the stream current, so that
+def _launch(device, stream, call):
+    """call(stream handle) with the device and the stream current, so that
     the tensors it makes belong to that stream."""
     if stream is None:
-        device = x.get_device()
-        if device == torch.cuda.current_device():
+        if device == _current_device():
             return call(_raw_stream(device))
         with torch.cuda.device(device):
             return call(_raw_stream(device))
-    if stream.device != x.device:
-        raise ValueError(f"the stream must be on {x.device}")
+    if stream.device.index != device:
+        raise ValueError(f"the stream must be on cuda:{device}")
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 
@@ -678,49 +679,54 @@ def _like(x):
 _plain_opts = {}
 
 
-def _opts_of(x, gate, cu_seqlens=None):
+def _opts_of(dtype, gate, cu_seqlens=None):
     if cu_seqlens is not None:
-        return _Opts(DTYPES[x.dtype], GATES[gate], cu_seqlens.data_ptr(),
-                     cu_seqlens.numel() - 1, ALGOS["auto"])
-    key = (x.dtype, gate)
-    opts = _plain_opts.get(key)
+        return ctypes.byref(_Opts(DTYPES[dtype], GATES[gate],
+                                  cu_seqlens.data_ptr(),
+                                  cu_seqlens.numel() - 1, ALGOS["auto"]))
+    opts = _plain_opts.get((dtype, gate))
     if opts is None:
-        opts = _plain_opts[key] = _Opts(DTYPES[x.dtype], GATES[gate], None, 0,
-                                        ALGOS["auto"])
+        opts = _plain_opts[dtype, gate] = ctypes.byref(
+            _Opts(DTYPES[dtype], GATES[gate], None, 0, ALGOS["auto"]))
     return opts
 
 
-def _linear_gate(x, log_alpha, gate):
-    """(gate, address of log_alpha)"""
+def _linear_gate(shape, device, log_alpha, gate):
+    """(gate, address of log_alpha) for x of this shape"""
+    if log_alpha is None:
+        if gate is not None and gate != "none":
+            raise ValueError("a gate needs log_alpha" if gate in GATES else
+                             f"gate must be one of {sorted(GATES)}")
+        return "none", None
     if gate is None:
-        gate = ("none" if log_alpha is None else
-                "scalar" if log_alpha.dim() == x.dim() - 1 else "channel")
-    if gate not in GATES:
+        gate = "scalar" if log_alpha.dim() == len(shape) - 1 else "channel"
+    elif gate not in GATES:
         raise ValueError(f"gate must be one of {sorted(GATES)}")
-    if (gate == "none") != (log_alpha is None):
-        raise ValueError("log_alpha must be given for a gate, and only then")
+    elif gate == "none":
+        raise ValueError("log_alpha needs a gate")
     return gate, _check("log_alpha", log_alpha,
-                        x.shape[:-1] if gate == "scalar" else x.shape,
-                        torch.float32, x)
+                        shape[:-1] if gate == "scalar" else shape,
+                        torch.float32, device)
 
 
 def _linear_args(x, log_alpha, initial_state, gate, cu_seqlens):
     if x.dim() != 4:
         raise ValueError("x must be [B, T, H, d]")
-    ldx = _activation("x", x, 2)
-    B, T, H, d = x.shape
-    nseq = B
+    shape, ldx, device = _activation(x, 2)
+    nseq, T, H, d = shape
     if cu_seqlens is not None:
-        if B != 1:
+        if nseq != 1:
             raise ValueError("packed sequences (cu_seqlens) need B = 1")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [num_seqs + 1]")
-        _check("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, x)
+        _check("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32,
+               device)
         nseq = cu_seqlens.numel() - 1
-    g, la = _linear_gate(x, log_alpha, gate)
-    s0 = _check("initial_state", initial_state, (nseq, H, d), torch.float32,
-                x)
-    return ldx, B, T, H, d, nseq, la, s0, _opts_of(x, g, cu_seqlens)
+    gate, la = _linear_gate(shape, device, log_alpha, gate)
+    states = (nseq, H, d)
+    s0 = _check("initial_state", initial_state, states, torch.float32, device)
+    return (shape, ldx, device, states, la, s0,
+            _opts_of(x.dtype, gate, cu_seqlens))
 
 
 def linear_fwd(x, log_alpha=None, initial_state=None, *,
@@ -738,30 +744,30 @@ def linear_fwd(x, log_alpha=None, initial_state=None, *,
     to ``linear_backward``.  final_state is None if not requested.
     """
     lib = load_library()
-    ldx, B, T, H, d, nseq, la, s0, opts = _linear_args(
+    shape, ldx, device, states, la, s0, opts = _linear_args(
         x, log_alpha, initial_state, gate, cu_seqlens)
-    _check("out", out, x.shape, x.dtype, x)
-    _check("final_state", final_state, (nseq, H, d), torch.float32, x)
+    B, T, H, d = shape
+    _check("out", out, shape, x.dtype, device)
+    _check("final_state", final_state, states, torch.float32, device)
 
     def call(handle):
         o = out if out is not None else _like(x)
         fin = final_state
         if fin is None and output_final_state:
-            fin = x.new_empty((nseq, H, d), dtype=torch.float32)
+            fin = x.new_empty(states, dtype=torch.float32)
         cs = None
         if output_chunk_states:
-            cs = x.new_empty((B * T // LINEAR_CHUNK + nseq, H, d),
+            cs = x.new_empty((B * T // LINEAR_CHUNK + states[0], H, d),
                              dtype=torch.float32)
         rc = lib.gdr_linear_fwd(
             x.data_ptr(), ldx, la, s0, o.data_ptr(),
             None if fin is None else fin.data_ptr(),
-            None if cs is None else cs.data_ptr(), B, T, H, d, handle,
-            ctypes.byref(opts))
+            None if cs is None else cs.data_ptr(), B, T, H, d, handle, opts)
         if rc != 0:
             raise GdrError(rc, "gdr_linear_fwd")
         return (o, fin, cs) if output_chunk_states else (o, fin)
 
-    return _launch(x, stream, call)
+    return _launch(device, stream, call)
 
 
 def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
@@ -777,13 +783,12 @@ def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
     lib = load_library()
     if x.dim() != 3:
         raise ValueError("x must be [N, H, d]")
-    ldx = _activation("x", x, 2)
-    shape = x.shape
-    g, la = _linear_gate(x, log_alpha, gate)
-    sin = _check("state", state, shape, torch.float32, x)
-    _check("out", out, shape, x.dtype, x)
-    _check("state_out", state_out, shape, torch.float32, x)
-    opts = _opts_of(x, g)
+    shape, ldx, device = _activation(x, 2)
+    gate, la = _linear_gate(shape, device, log_alpha, gate)
+    sin = _check("state", state, shape, torch.float32, device)
+    _check("out", out, shape, x.dtype, device)
+    _check("state_out", state_out, shape, torch.float32, device)
+    opts = _opts_of(x.dtype, gate)
 
     def call(handle):
         o = out if out is not None else _like(x)
@@ -791,13 +796,12 @@ def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
         if so is None:
             so = x.new_empty(shape, dtype=torch.float32)
         rc = lib.gdr_linear_step(x.data_ptr(), ldx, la, sin, so.data_ptr(),
-                                 o.data_ptr(), shape[0], shape[1], shape[2],
-                                 handle, ctypes.byref(opts))
+                                 o.data_ptr(), *shape, handle, opts)
         if rc != 0:
             raise GdrError(rc, "gdr_linear_step")
         return o, so
 
-    return _launch(x, stream, call)
+    return _launch(device, stream, call)
 
 
 def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
@@ -811,48 +815,48 @@ def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
     tensors dx (the dtype of x), dlog_alpha (fp32; None without a gate) and
     dinitial_state (fp32; None unless requested)."""
     lib = load_library()
-    ldx, B, T, H, d, nseq, la, s0, opts = _linear_args(
+    shape, ldx, device, states, la, s0, opts = _linear_args(
         x, log_alpha, initial_state, gate, cu_seqlens)
-    do = _check("d_out", d_out, x.shape, x.dtype, x)
+    B, T, H, d = shape
+    do = _check("d_out", d_out, shape, x.dtype, device)
     if do is None:
         raise ValueError("d_out must be given")
-    ds = _check("d_final_state", d_final_state, (nseq, H, d), torch.float32,
-                x)
+    ds = _check("d_final_state", d_final_state, states, torch.float32, device)
     cs = _check("chunk_states", chunk_states,
-                (B * T // LINEAR_CHUNK + nseq, H, d), torch.float32, x)
+                (B * T // LINEAR_CHUNK + states[0], H, d), torch.float32,
+                device)
 
     def call(handle):
         dx = _like(x)
         gla = None if log_alpha is None else torch.empty_like(log_alpha)
-        gs0 = (x.new_empty((nseq, H, d), dtype=torch.float32)
+        gs0 = (x.new_empty(states, dtype=torch.float32)
                if need_initial_state_grad else None)
         rc = lib.gdr_linear_backward(
             x.data_ptr(), ldx, la, s0, cs, do, ds, dx.data_ptr(),
             None if gla is None else gla.data_ptr(),
-            None if gs0 is None else gs0.data_ptr(), B, T, H, d, handle,
-            ctypes.byref(opts))
+            None if gs0 is None else gs0.data_ptr(), B, T, H, d, handle, opts)
         if rc != 0:
             raise GdrError(rc, "gdr_linear_backward")
         return dict(dx=dx, dlog_alpha=gla, dinitial_state=gs0)
 
-    return _launch(x, stream, call)
+    return _launch(device, stream, call)
 
 
 def _norm_args(x, weight):
-    """(ldx, number of tokens, heads, channels, the parameters' shape, the
-    weight's address)."""
-    if weight is not None and weight.dim() not in (1, 2):
-        raise ValueError("weight must be [d] or [H, d]")
-    inner = 1 if weight is None else weight.dim()
-    if x.dim() < inner:
-        raise ValueError("x must be [.., d], or [.., H, d] with a weight "
-                         "[H, d]")
-    ldx = _activation("x", x, inner)
-    shape = x.shape[x.dim() - inner:]
-    w = _check("weight", weight, shape, torch.float32, x)
-    H, d = (1, shape[0]) if inner == 1 else shape
-    ntok = x.numel() // (H * d) if H * d else 0
-    return ldx, ntok, H, d, shape, w
+    """(x's shape, ldx, device, (number of tokens, heads, channels), the
+    parameters' shape, the weight's address)."""
+    inner = 1
+    if weight is not None:
+        inner = weight.dim()
+        if inner != 1 and inner != 2:
+            raise ValueError("weight must be [d] or [H, d]")
+    shape, ldx, device = _activation(x, inner)
+    pshape = shape[-inner:]
+    w = _check("weight", weight, pshape, torch.float32, device)
+    d = shape[-1]
+    H = 1 if inner == 1 else shape[-2]
+    n = x.numel()
+    return (shape, ldx, device, (n // (H * d) if n else 0, H, d), pshape, w)
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
@@ -865,19 +869,19 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
     lib = load_library()
     if bias is not None and weight is None:
         raise ValueError("a bias needs a weight")
-    ldx, ntok, H, d, shape, w = _norm_args(x, weight)
-    b = _check("bias", bias, shape, torch.float32, x)
-    _check("out", out, x.shape, x.dtype, x)
+    shape, ldx, device, sizes, pshape, w = _norm_args(x, weight)
+    b = _check("bias", bias, pshape, torch.float32, device)
+    _check("out", out, shape, x.dtype, device)
 
     def call(handle):
         o = out if out is not None else _like(x)
-        rc = lib.gdr_layer_norm(x.data_ptr(), ldx, w, b, o.data_ptr(), ntok,
-                                H, d, eps, DTYPES[x.dtype], handle)
+        rc = lib.gdr_layer_norm(x.data_ptr(), ldx, w, b, o.data_ptr(), *sizes,
+                                eps, DTYPES[x.dtype], handle)
         if rc != 0:
             raise GdrError(rc, "gdr_layer_norm")
         return o
 
-    return _launch(x, stream, call)
+    return _launch(device, stream, call)
 
 
 def layer_norm_backward(x, weight, d_out, *, eps: float = 1e-5,
@@ -887,8 +891,8 @@ def layer_norm_backward(x, weight, d_out, *, eps: float = 1e-5,
     Returns a dict of CUDA tensors dx (the dtype of x), dweight and dbias
     (fp32, the shape of weight; None without a weight or if not needed)."""
     lib = load_library()
-    ldx, ntok, H, d, shape, w = _norm_args(x, weight)
-    dy = _check("d_out", d_out, x.shape, x.dtype, x)
+    shape, ldx, device, sizes, _, w = _norm_args(x, weight)
+    dy = _check("d_out", d_out, shape, x.dtype, device)
     if dy is None:
         raise ValueError("d_out must be given")
 
@@ -900,13 +904,13 @@ def layer_norm_backward(x, weight, d_out, *, eps: float = 1e-5,
         rc = lib.gdr_layer_norm_backward(
             x.data_ptr(), ldx, w, dy, dx.data_ptr(),
             None if dw is None else dw.data_ptr(),
-            None if db is None else db.data_ptr(), ntok, H, d, eps,
+            None if db is None else db.data_ptr(), *sizes, eps,
             DTYPES[x.dtype], handle)
         if rc != 0:
             raise GdrError(rc, "gdr_layer_norm_backward")
         return dict(dx=dx, dweight=dw, dbias=db)
 
-    return _launch(x, stream, call)
+    return _launch(device, stream, call)
 
 
 def device_error(stream=None, clear: bool = True) -> int:

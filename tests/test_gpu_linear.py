@@ -340,6 +340,33 @@ def test_other_stream_and_repeatable():
         assert all(torch.equal(ga[k], gb[k]) for k in ga)
 
 
+def test_two_streams_at_once():
+    """Training steps with scratch, in flight on two streams together."""
+    cases = [inputs(1, 3000, 2, 40, "fp32", "scalar", seed=s) for s in (1, 2)]
+    want = [gdr.linear_backward(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = [gdr.linear_backward(*c, stream=s)
+               for c, s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for w, g in zip(want, got):
+            assert all(torch.equal(w[k], g[k]) for k in w)
+
+
+@pytest.mark.parametrize("T", [20, 300, 3000])
+def test_growing_states(T):
+    """log_alpha above 0 is outside what is expected, but means what it
+    says."""
+    x, la, s0, dO, dS = inputs(1, T, 1, 36, "fp32", "channel")
+    la = -la * (3.0 / T)
+    out, fin = gdr.linear_fwd(x, la, s0)
+    res = gdr.linear_backward(x, la, s0, dO, dS)
+    torch.cuda.synchronize()
+    check_fwd(x, la, s0, out, fin)
+    check_bwd(x, la, s0, dO, dS, res)
+
+
 def test_captured_steps_share_nothing():
     """Two captured training steps with scratch, replayed in turn on new
     inputs, and the eager calls agree bit for bit."""
