@@ -676,6 +676,13 @@ def _like(x):
     return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
+def _state_like(x, shape, state):
+    """An fp32 tensor of this shape; `state`: one such, or None."""
+    if state is not None:
+        return torch.empty_like(state)
+    return torch.empty(shape, dtype=torch.float32, device=x.device)
+
+
 _plain_opts = {}
 
 
@@ -754,11 +761,11 @@ def linear_fwd(x, log_alpha=None, initial_state=None, *,
         o = out if out is not None else _like(x)
         fin = final_state
         if fin is None and output_final_state:
-            fin = x.new_empty(states, dtype=torch.float32)
+            fin = _state_like(x, states, initial_state)
         cs = None
         if output_chunk_states:
-            cs = x.new_empty((B * T // LINEAR_CHUNK + states[0], H, d),
-                             dtype=torch.float32)
+            cs = _state_like(
+                x, (B * T // LINEAR_CHUNK + states[0], H, d), None)
         rc = lib.gdr_linear_fwd(
             x.data_ptr(), ldx, la, s0, o.data_ptr(),
             None if fin is None else fin.data_ptr(),
@@ -794,7 +801,7 @@ def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
         o = out if out is not None else _like(x)
         so = state_out if state_out is not None else state
         if so is None:
-            so = x.new_empty(shape, dtype=torch.float32)
+            so = _state_like(x, shape, None)
         rc = lib.gdr_linear_step(x.data_ptr(), ldx, la, sin, so.data_ptr(),
                                  o.data_ptr(), *shape, handle, opts)
         if rc != 0:
@@ -829,7 +836,7 @@ def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
     def call(handle):
         dx = _like(x)
         gla = None if log_alpha is None else torch.empty_like(log_alpha)
-        gs0 = (x.new_empty(states, dtype=torch.float32)
+        gs0 = (_state_like(x, states, initial_state)
                if need_initial_state_grad else None)
         rc = lib.gdr_linear_backward(
             x.data_ptr(), ldx, la, s0, cs, do, ds, dx.data_ptr(),

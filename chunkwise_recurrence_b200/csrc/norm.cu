@@ -99,17 +99,18 @@ __device__ __forceinline__ void store(float *p, const float *f) {
   else
     *p = f[0];
 }
-// Sums two values over the G threads of each group.  G <= 32: within the
-// warp; else over the group's warps through shared memory, the group meeting
-// at its own barrier (`sm` is not in use by an earlier call that some thread
-// may still be reading).
-template <int G>
+// Sums one or two values over the G threads of each group.  G <= 32: within
+// the warp; else over the group's warps through shared memory, the group
+// meeting at its own barrier (`sm` is not in use by an earlier call that some
+// thread may still be reading).
+template <int G, bool TWO>
 __device__ __forceinline__ void group_sum(float &a, float &b, float2 *sm) {
-#pragma unroll
-  for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) {
+  auto fold = [&](int o) {
     a += __shfl_xor_sync(~0u, a, o);
-    b += __shfl_xor_sync(~0u, b, o);
-  }
+    if constexpr (TWO) b += __shfl_xor_sync(~0u, b, o);
+  };
+#pragma unroll
+  for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) fold(o);
   if constexpr (G > 32) {
     constexpr int NW = G / 32;
     const int w = threadIdx.x >> 5;
@@ -119,15 +120,15 @@ __device__ __forceinline__ void group_sum(float &a, float &b, float2 *sm) {
     if constexpr (NW <= 8) {
       a = b = 0.f;
 #pragma unroll
-      for (int j = 0; j < NW; ++j) a += g[j].x, b += g[j].y;
+      for (int j = 0; j < NW; ++j) {
+        a += g[j].x;
+        if constexpr (TWO) b += g[j].y;
+      }
     } else {
       const float2 t = g[threadIdx.x % NW];
       a = t.x, b = t.y;
 #pragma unroll
-      for (int o = NW / 2; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(~0u, a, o);
-        b += __shfl_xor_sync(~0u, b, o);
-      }
+      for (int o = NW / 2; o > 0; o >>= 1) fold(o);
     }
   }
 }
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kFwdBlock
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i) s = add2(s, r[0].p[i]);
     float mean = total(s), none = 0.f;
-    group_sum<G>(mean, none, sm[0]);
+    group_sum<G, false>(mean, none, sm[0]);
     mean *= inv;
     Row c;
 #pragma unroll
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kFwdBlock
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i) s = fma2(c.p[i], c.p[i], s);
     float var = total(s);
-    group_sum<G>(var, none, sm[1]);
+    group_sum<G, false>(var, none, sm[1]);
     const Pair rstd = both(1.f / sqrtf(var * inv + eps));
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i)
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kBwdBlock
       t = fma2(r[1].p[i], wr.p[i], t);
     }
     float mean = total(s), m1 = total(t);
-    group_sum<G>(mean, m1, sm[0]);
+    group_sum<G, true>(mean, m1, sm[0]);
     mean *= inv;
     m1 *= inv;
 #pragma unroll
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kBwdBlock
       t = fma2(mul2(r[1].p[i], wr.p[i]), r[0].p[i], t);
     }
     float var = total(s), m2 = total(t);
-    group_sum<G>(var, m2, sm[1]);
+    group_sum<G, true>(var, m2, sm[1]);
     const float rstd = 1.f / sqrtf(var * inv + eps);
     m2 *= inv * rstd;
     Row o;
