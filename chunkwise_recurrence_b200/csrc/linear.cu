@@ -581,12 +581,17 @@ struct Rows {
                                        int have) const {
     src += lane();
     dst += lane();
-    if (lane() >= n) have = 0;
     float v[ROWS];
+    if (have == ROWS && n == kRow) {
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      v[r] = 0.f;
-      if (r < have) v[r] = __ldg(src + (long long)r * ld);
+      for (int r = 0; r < ROWS; ++r) v[r] = __ldg(src + (long long)r * ld);
+    } else {
+      if (lane() >= n) have = 0;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        v[r] = 0.f;
+        if (r < have) v[r] = __ldg(src + (long long)r * ld);
+      }
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) dst[r * 32] = v[r];
@@ -599,29 +604,36 @@ struct Rows {
     auto word = [&](int r, int j, int &bytes) {
       const uintptr_t at =
           reinterpret_cast<uintptr_t>(src + (long long)r * ld);
-      bytes = (int)(at & 2) + 2 * n - 4 * j;
+      bytes = r < have ? (int)(at & 2) + 2 * n - 4 * j : 0;
       return reinterpret_cast<const char *>(at & ~(uintptr_t)3) + 4 * j;
     };
-    auto read = [&](const char *p, bool ok, int bytes) {
+    auto read = [&](const char *p, int bytes) {
       uint32_t v = 0;
-      if (ok && bytes >= 4) v = __ldg(reinterpret_cast<const uint32_t *>(p));
-      if (ok && bytes == 2)
-        v = __ldg(reinterpret_cast<const unsigned short *>(p));
-      return __uint_as_float(v);
+      if (bytes >= 4) v = __ldg(reinterpret_cast<const uint32_t *>(p));
+      if (bytes == 2) v = __ldg(reinterpret_cast<const unsigned short *>(p));
+      return v;
     };
     const int r0 = lane() / 16, j = lane() % 16;
     int bytes, bytes1;
     const char *p = word(r0, j, bytes);
     const char *p1 = word(lane(), 16, bytes1);
-    float v[ROWS / 2];
+    uint32_t *d = reinterpret_cast<uint32_t *>(dst);
+    uint32_t v[ROWS / 2];
+    if (have == ROWS && n == kRow) {       // (then words 0 .. 15 are whole)
 #pragma unroll
-    for (int r = 0; r < ROWS; r += 2)
-      v[r / 2] = read(p + (long long)r * (2 * ld), r + r0 < have, bytes);
-    const float v1 = read(p1, lane() < have, bytes1);
-    float *d = dst + r0 * kPitch + j;
+      for (int r = 0; r < ROWS; r += 2)
+        v[r / 2] = __ldg(
+            reinterpret_cast<const uint32_t *>(p + (long long)r * (2 * ld)));
+    } else {
+#pragma unroll
+      for (int r = 0; r < ROWS; r += 2)
+        v[r / 2] = read(p + (long long)r * (2 * ld),
+                        r + r0 < have ? bytes : 0);
+    }
+    d[lane() * kPitch + 16] = read(p1, bytes1);
+    d += r0 * kPitch + j;
 #pragma unroll
     for (int r = 0; r < ROWS; r += 2) d[r * kPitch] = v[r / 2];
-    dst[lane() * kPitch + 16] = v1;
   }
   // brings row `lane` of the next step's tile into L2
   template <typename E>
@@ -708,7 +720,15 @@ struct Rows {
     T *o = out + (long long)t0 * ldd + lane();
     float *og = dla + (long long)t0 * ldd + lane();
     __syncwarp();
+    if (n == kRow && end - t0 >= kRow) {
 #pragma unroll
+      for (int r = 0; r < kRow; ++r) {
+        o[(long long)r * ldd] = d[r * kRow];
+        if constexpr (BWD && kGate) og[(long long)r * ldd] = g[r * kRow];
+      }
+      return;
+    }
+#pragma unroll 4
     for (int r = 0; r < kRow; ++r)
       if (r < have) {
         o[(long long)r * ldd] = d[r * kRow];
