@@ -1019,6 +1019,27 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
 
 // ---------------------------------------------------------------- backward
 
+// Sums v[0 .. 7] over the LANES (8 or 16) threads of a token run, thread c of
+// which ends with one of the sums in v[0]; returns which.  In every round
+// each thread hands half of its values to a partner and adds the partner's
+// to the other half.
+template <int LANES>
+__device__ __forceinline__ int sum_tokens(float (&v)[kR], int c) {
+  int which = 0;
+#pragma unroll
+  for (int n = kR / 2, o = LANES / 2; n > 0; n >>= 1, o >>= 1) {
+    const bool up = c & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(~0u, give, o);
+    }
+    which += up ? n : 0;
+  }
+  if constexpr (LANES == 16) v[0] += __shfl_xor_sync(~0u, v[0], 1);
+  return which;
+}
+
 // From the last token to the first.  Every thread runs h forward over its
 // tokens from their chunk state, leaving alpha_t h_{t-1} in registers; then c
 // runs backward through the same joins as the forward pass.
@@ -1130,6 +1151,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
       for (int v = 0; v < kV; ++v) cy[v] = jt.in[w][c * kV + v];
     }
     enter<LANES, GV, GATE>(cy, ex, runs);
+    float dl8[kR];                       // G alpha h, summed over channels
     auto again = [&](auto tc) {
 #pragma unroll
       for (int r = kR - 1; r >= 0; --r) {
@@ -1152,25 +1174,28 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
             in.put_la(slots, r, dl);
         }
         if constexpr (GATE == GDR_GATE_SCALAR) {
-          // the head's share of this tile, added in a fixed order
-          float dl = 0.f;
-#pragma unroll
-          for (int v = 0; v < kV; ++v) dl = fmaf(cy[v], ah[r][v], dl);
-#pragma unroll
-          for (int o = LANES / 2; o > 0; o >>= 1)
-            dl += __shfl_xor_sync(~0u, dl, o);
-          if (n && c == 0) {
-            if (p.nct == 1)
-              p.dla[(tok + r) * p.H + q.head] = dl;
-            else
-              p.part[((long long)q.ct * p.ntok + tok + r) * p.H + q.head] =
-                  dl;
-          }
+          Pair t = mul2(pair(cy[0], cy[1]), pair(ah[r][0], ah[r][1]));
+          t = fma2(pair(cy[2], cy[3]), pair(ah[r][2], ah[r][3]), t);
+          float lo, hi;
+          split(t, lo, hi);
+          dl8[r] = lo + hi;
         }
         decay_all<GV, GATE, tc.value>(cy, m[r]);
       }
     };
     if (tight) again(Bool<true>{}); else again(Bool<false>{});
+    if constexpr (GATE == GDR_GATE_SCALAR) {
+      // the head's share of this tile, added over the threads of a token in a
+      // fixed order; each thread ends with one token's sum
+      const int r = sum_tokens<LANES>(dl8, c);
+      if (t + r < end && (LANES == 8 || c % 2 == 0)) {
+        const long long to = tok + r;
+        if (p.nct == 1)
+          p.dla[to * p.H + q.head] = dl8[0];
+        else
+          p.part[((long long)q.ct * p.ntok + to) * p.H + q.head] = dl8[0];
+      }
+    }
     if constexpr (!VEC) in.flush(slots);
     xo -= (long long)kBlock * nc * p.D;
   }
