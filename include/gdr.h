@@ -1,6 +1,7 @@
 /*
  * gdr.h -- C ABI of libgdr: the chunkwise-parallel forward pass of the gated
- * delta rule on one NVIDIA B200 (sm_100a).
+ * delta rule on one NVIDIA B200 (sm_100a), and beside it a gated linear
+ * recurrence and layer normalisation.
  *
  * The operation (per sequence and head; tokens t in order; state S is dk x dv):
  *
@@ -620,8 +621,17 @@ GDR_API gdr_status gdr_efla_beta_backward(const void *k, const float *beta,
  *
  * Sizes: B, T, H >= 0, d >= 1, H <= 65535, H d <= 2^24; at most 2^28
  * (sequence, 32-channel) pairs.  State and sums are fp32; out is rounded
- * once.  opts->algo must be AUTO.  One launch, no scratch; results do not
- * depend on scheduling.
+ * once.  ldx < 2^30.  opts->algo must be AUTO.  One launch, no scratch;
+ * results do not depend on scheduling.  Where a sequence is cut across blocks
+ * they wait for one another's states, bounded: an expired wait is reported
+ * by gdr_device_error as GDR_ERR_TIMEOUT, and the results are not to be used
+ * (the environment variable GDR_FAULT_INJECT_LINEAR_TIMEOUT=1 makes every such
+ * wait expire, for tests of that path).  Fastest where H d and ldx are
+ * multiples of 4 (with a SCALAR decay d as well).
+ *
+ * Returns GDR_ERR_INVALID_ARGUMENT for null or misaligned pointers,
+ * overlapping buffers and inconsistent sizes, GDR_ERR_UNSUPPORTED for sizes
+ * beyond those above, GDR_ERR_CUDA if the launch fails.
  */
 #define GDR_LINEAR_CHUNK 8
 
@@ -639,7 +649,8 @@ GDR_API gdr_status gdr_linear_fwd(const void *x, long long ldx,
  * x [N][H][d] dtype, rows ldx apart; log_alpha NULL, [N][H] or [N][H][d];
  * state_in [N][H][d] fp32 or NULL (zero); state_out [N][H][d] fp32 (written),
  * which may be state_in itself; out [N][H][d] dtype (written).  No
- * cu_seqlens.  Limits and status codes as for gdr_linear_fwd.
+ * cu_seqlens.  One launch, no waits.  Limits and status codes as for
+ * gdr_linear_fwd.
  */
 GDR_API gdr_status gdr_linear_step(const void *x, long long ldx,
                                    const float *log_alpha,
@@ -667,8 +678,9 @@ GDR_API gdr_status gdr_linear_step(const void *x, long long ldx,
  *   d_initial_state [N][H][d] fp32 (written), or NULL to skip.
  * Rows outside every sequence are left as they were.  Scratch, only where
  * needed: the chunk states if they are not given (a forward pass more), and
- * for SCALAR with d > 32 (d + 31) / 32 copies of d_log_alpha; stream-ordered
- * from the library's pool, GDR_ERR_OUT_OF_MEMORY on failure.
+ * for SCALAR with d > 32 up to (d + 31) / 32 copies of d_log_alpha;
+ * stream-ordered from the library's pool, GDR_ERR_OUT_OF_MEMORY on failure.
+ * Waits and the other status codes as for gdr_linear_fwd.
  */
 GDR_API gdr_status gdr_linear_backward(
     const void *x, long long ldx, const float *log_alpha,
@@ -689,7 +701,9 @@ GDR_API gdr_status gdr_linear_backward(
  * zeros); out [ntok][H][d] in `dtype` (written; must not overlap the rest).
  * 1 <= d <= 16384, H <= 65535, ntok H < 2^31, eps >= 0.  ntok H == 0 is a
  * no-op.  Statistics in fp32, the variance from distances to the mean; y is
- * rounded once.  One launch, no scratch.
+ * rounded once.  A row with an infinity or NaN gives NaN; a constant row with
+ * eps = 0 too (0 / 0).  One launch, no scratch.  Status codes as for
+ * gdr_linear_fwd.
  */
 GDR_API gdr_status gdr_layer_norm(const void *x, long long ldx,
                                   const float *weight, const float *bias,
@@ -705,8 +719,9 @@ GDR_API gdr_status gdr_layer_norm(const void *x, long long ldx,
  * [ntok][H][d] in `dtype`; dx the same (written); d_weight and d_bias [H][d]
  * fp32 (written, summed over the tokens in fp32 and in a fixed order), each
  * NULL to skip.  With no token dx is empty and the sums are zero.  Scratch
- * for d_weight and d_bias: up to 444 rows of H d floats each, stream-ordered
- * from the library's pool; GDR_ERR_OUT_OF_MEMORY on failure.
+ * for d_weight and d_bias, but for few tokens: up to 296 rows of H d floats
+ * each, stream-ordered from the library's pool; GDR_ERR_OUT_OF_MEMORY on
+ * failure.  A row with an infinity or NaN gives NaN in its dx and in the sums.
  */
 GDR_API gdr_status gdr_layer_norm_backward(
     const void *x, long long ldx, const float *weight, const void *d_out,
@@ -717,8 +732,9 @@ GDR_API gdr_status gdr_layer_norm_backward(
  * gdr_device_error -- synchronise `stream`, then read (and clear if `clear`)
  * the library's sticky device-side error word for the current device.
  * Returns GDR_OK if no kernel has reported an error, GDR_ERR_TIMEOUT if a
- * bounded wait expired (the fused kernel's, or the decode step's wait for its
- * state tile), GDR_ERR_RANGE if the fused kernel produced a
+ * bounded wait expired (the fused kernel's, the decode step's wait for its
+ * state tile, or the linear recurrence's for another block's state),
+ * GDR_ERR_RANGE if the fused kernel produced a
  * non-finite output or final state (an input or intermediate beyond the
  * fp16 operand range, |x| > 65504, or a NaN input) or, for the channel gate,
  * met such an input,
