@@ -11,6 +11,8 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -28,6 +30,7 @@ __all__ = ["chunk_fwd", "chunk_fwd_host", "chunk_fwd_noalloc",
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdr.so")
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
 
 GATES = {"none": 0, "scalar": 1, "channel": 2}
 ALGOS = {"auto": 0, "staged": 1, "fused_tc": 2, "recurrent": 3}
@@ -593,147 +596,35 @@ def efla_beta_backward(k, beta, d_beta_prime, dk, *, d_beta=None,
 
 # ---------------------------------------------------------------------------
 # Linear recurrence and layer normalisation.  Unlike the entries above, these
-# check every tensor (ValueError) before they call the library.
+# check every tensor (ValueError) before they call the library, and they do it
+# in a compiled extension (csrc/binding.cpp), since a decoding step is short.
 
-def _activation(x, inner):
-    """Checks a device tensor of activations [.., inner dims] whose inner
-    dimensions are contiguous and whose tokens are evenly spaced; returns
-    (shape, distance between tokens in elements, device)."""
-    shape = x.shape
-    outer = len(shape) - inner
-    if outer < 0:
-        raise ValueError(f"x must have at least {inner} dimension(s)")
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    if x.dtype not in DTYPES:
-        raise ValueError("x must be bfloat16 or float32")
-    step = shape[-1] if inner == 1 else shape[-1] * shape[-2]
-    if x.is_contiguous():
-        return shape, step, x.get_device()
-    strides = x.stride()
-    n = 1
-    for i in range(len(shape) - 1, outer - 1, -1):
-        if shape[i] != 1 and strides[i] != n:
-            raise ValueError(f"x: the last {inner} dimension(s) must be "
-                             "contiguous")
-        n *= shape[i]
-    ld, rows = None, 1
-    for i in range(outer - 1, -1, -1):
-        if shape[i] == 1:
-            continue
-        if ld is None:
-            ld = strides[i]
-            if ld < step:
-                raise ValueError("x: tokens must not overlap")
-        elif strides[i] != ld * rows:
-            raise ValueError("x: tokens must be evenly spaced")
-        rows *= shape[i]
-    return shape, step if ld is None else ld, x.get_device()
+_native = None
 
 
-def _check(name, t, shape, dtype, device):
-    """Checks another tensor of a call whose activations are on `device`;
-    returns its address (None for None)."""
-    if t is None:
-        return None
-    if (t.shape == shape and t.dtype is dtype and t.is_contiguous() and
-            t.get_device() == device):
-        return t.data_ptr()
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, "
-                         f"not {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on cuda:{device}, not {t.device}")
-    raise ValueError(f"{name} must be contiguous")
+def _load_native():
+    """Load the extension (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        load_library()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                f"{BINDING_PATH} is missing: build it with "
+                "`python -m chunkwise_recurrence_b200.build` (needs g++)")
+        name = __name__ + "._binding"
+        loader = importlib.machinery.ExtensionFileLoader(name, BINDING_PATH)
+        spec = importlib.util.spec_from_loader(name, loader)
+        _native = importlib.util.module_from_spec(spec)
+        loader.exec_module(_native)
+    return _native
 
 
-# (the handle of the current stream without a torch.cuda.Stream around it,
-# where this build of PyTorch has it)
-_raw_stream = getattr(
-    torch._C, "_cuda_getCurrentRawStream",
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
-_current_device = torch.cuda.current_device
-
-
-def _launch(device, stream, call):
-    """call(stream handle) with the device and the stream current, so that
-    the tensors it makes belong to that stream."""
-    if stream is None:
-        if device == _current_device():
-            return call(_raw_stream(device))
-        with torch.cuda.device(device):
-            return call(_raw_stream(device))
-    if stream.device.index != device:
-        raise ValueError(f"the stream must be on cuda:{device}")
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
-
-
-def _like(x):
-    """A contiguous tensor of x's shape and type."""
-    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
-
-
-def _state_like(x, shape, state):
-    """An fp32 tensor of this shape; `state`: one such, or None."""
-    if state is not None:
-        return torch.empty_like(state)
-    return torch.empty(shape, dtype=torch.float32, device=x.device)
-
-
-_plain_opts = {}
-
-
-def _opts_of(dtype, gate, cu_seqlens=None):
-    if cu_seqlens is not None:
-        return ctypes.byref(_Opts(DTYPES[dtype], GATES[gate],
-                                  cu_seqlens.data_ptr(),
-                                  cu_seqlens.numel() - 1, ALGOS["auto"]))
-    opts = _plain_opts.get((dtype, gate))
-    if opts is None:
-        opts = _plain_opts[dtype, gate] = ctypes.byref(
-            _Opts(DTYPES[dtype], GATES[gate], None, 0, ALGOS["auto"]))
-    return opts
-
-
-def _linear_gate(shape, device, log_alpha, gate):
-    """(gate, address of log_alpha) for x of this shape"""
-    if log_alpha is None:
-        if gate is not None and gate != "none":
-            raise ValueError("a gate needs log_alpha" if gate in GATES else
-                             f"gate must be one of {sorted(GATES)}")
-        return "none", None
-    if gate is None:
-        gate = "scalar" if log_alpha.dim() == len(shape) - 1 else "channel"
-    elif gate not in GATES:
-        raise ValueError(f"gate must be one of {sorted(GATES)}")
-    elif gate == "none":
-        raise ValueError("log_alpha needs a gate")
-    return gate, _check("log_alpha", log_alpha,
-                        shape[:-1] if gate == "scalar" else shape,
-                        torch.float32, device)
-
-
-def _linear_args(x, log_alpha, initial_state, gate, cu_seqlens):
-    if x.dim() != 4:
-        raise ValueError("x must be [B, T, H, d]")
-    shape, ldx, device = _activation(x, 2)
-    nseq, T, H, d = shape
-    if cu_seqlens is not None:
-        if nseq != 1:
-            raise ValueError("packed sequences (cu_seqlens) need B = 1")
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError("cu_seqlens must be [num_seqs + 1]")
-        _check("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32,
-               device)
-        nseq = cu_seqlens.numel() - 1
-    gate, la = _linear_gate(shape, device, log_alpha, gate)
-    states = (nseq, H, d)
-    s0 = _check("initial_state", initial_state, states, torch.float32, device)
-    return (shape, ldx, device, states, la, s0,
-            _opts_of(x.dtype, gate, cu_seqlens))
+def _on(x, stream):
+    """Makes `stream` current, so that the call launches there and its results
+    belong to it."""
+    if stream.device != x.device:
+        raise ValueError(f"the stream must be on {x.device}")
+    return torch.cuda.stream(stream)
 
 
 def linear_fwd(x, log_alpha=None, initial_state=None, *,
@@ -750,31 +641,19 @@ def linear_fwd(x, log_alpha=None, initial_state=None, *,
     final_state, chunk_states) with ``output_chunk_states``: pass the latter
     to ``linear_backward``.  final_state is None if not requested.
     """
-    lib = load_library()
-    shape, ldx, device, states, la, s0, opts = _linear_args(
-        x, log_alpha, initial_state, gate, cu_seqlens)
-    B, T, H, d = shape
-    _check("out", out, shape, x.dtype, device)
-    _check("final_state", final_state, states, torch.float32, device)
-
-    def call(handle):
-        o = out if out is not None else _like(x)
-        fin = final_state
-        if fin is None and output_final_state:
-            fin = _state_like(x, states, initial_state)
-        cs = None
-        if output_chunk_states:
-            cs = _state_like(
-                x, (B * T // LINEAR_CHUNK + states[0], H, d), None)
-        rc = lib.gdr_linear_fwd(
-            x.data_ptr(), ldx, la, s0, o.data_ptr(),
-            None if fin is None else fin.data_ptr(),
-            None if cs is None else cs.data_ptr(), B, T, H, d, handle, opts)
-        if rc != 0:
-            raise GdrError(rc, "gdr_linear_fwd")
-        return (o, fin, cs) if output_chunk_states else (o, fin)
-
-    return _launch(device, stream, call)
+    if stream is not None:
+        with _on(x, stream):
+            return linear_fwd(
+                x, log_alpha, initial_state, gate=gate, cu_seqlens=cu_seqlens,
+                out=out, final_state=final_state,
+                output_final_state=output_final_state,
+                output_chunk_states=output_chunk_states)
+    r = (_native or _load_native()).linear_fwd(
+        x, log_alpha, initial_state, gate, cu_seqlens, out, final_state,
+        output_final_state, output_chunk_states)
+    if r.__class__ is int:
+        raise GdrError(r, "gdr_linear_fwd")
+    return r
 
 
 def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
@@ -787,28 +666,15 @@ def linear_step(x, log_alpha=None, state=None, *, out=None, state_out=None,
     ``state`` itself (an in-place update) when a state is given, else a new
     tensor.  Returns (out [N, H, d], state_out).
     """
-    lib = load_library()
-    if x.dim() != 3:
-        raise ValueError("x must be [N, H, d]")
-    shape, ldx, device = _activation(x, 2)
-    gate, la = _linear_gate(shape, device, log_alpha, gate)
-    sin = _check("state", state, shape, torch.float32, device)
-    _check("out", out, shape, x.dtype, device)
-    _check("state_out", state_out, shape, torch.float32, device)
-    opts = _opts_of(x.dtype, gate)
-
-    def call(handle):
-        o = out if out is not None else _like(x)
-        so = state_out if state_out is not None else state
-        if so is None:
-            so = _state_like(x, shape, None)
-        rc = lib.gdr_linear_step(x.data_ptr(), ldx, la, sin, so.data_ptr(),
-                                 o.data_ptr(), *shape, handle, opts)
-        if rc != 0:
-            raise GdrError(rc, "gdr_linear_step")
-        return o, so
-
-    return _launch(device, stream, call)
+    if stream is not None:
+        with _on(x, stream):
+            return linear_step(x, log_alpha, state, out=out,
+                               state_out=state_out, gate=gate)
+    r = (_native or _load_native()).linear_step(
+        x, log_alpha, state, out, state_out, gate)
+    if r.__class__ is int:
+        raise GdrError(r, "gdr_linear_step")
+    return r
 
 
 def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
@@ -821,49 +687,18 @@ def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
     it for these inputs, or None (computed again).  Returns a dict of CUDA
     tensors dx (the dtype of x), dlog_alpha (fp32; None without a gate) and
     dinitial_state (fp32; None unless requested)."""
-    lib = load_library()
-    shape, ldx, device, states, la, s0, opts = _linear_args(
-        x, log_alpha, initial_state, gate, cu_seqlens)
-    B, T, H, d = shape
-    do = _check("d_out", d_out, shape, x.dtype, device)
-    if do is None:
-        raise ValueError("d_out must be given")
-    ds = _check("d_final_state", d_final_state, states, torch.float32, device)
-    cs = _check("chunk_states", chunk_states,
-                (B * T // LINEAR_CHUNK + states[0], H, d), torch.float32,
-                device)
-
-    def call(handle):
-        dx = _like(x)
-        gla = None if log_alpha is None else torch.empty_like(log_alpha)
-        gs0 = (_state_like(x, states, initial_state)
-               if need_initial_state_grad else None)
-        rc = lib.gdr_linear_backward(
-            x.data_ptr(), ldx, la, s0, cs, do, ds, dx.data_ptr(),
-            None if gla is None else gla.data_ptr(),
-            None if gs0 is None else gs0.data_ptr(), B, T, H, d, handle, opts)
-        if rc != 0:
-            raise GdrError(rc, "gdr_linear_backward")
-        return dict(dx=dx, dlog_alpha=gla, dinitial_state=gs0)
-
-    return _launch(device, stream, call)
-
-
-def _norm_args(x, weight):
-    """(x's shape, ldx, device, (number of tokens, heads, channels), the
-    parameters' shape, the weight's address)."""
-    inner = 1
-    if weight is not None:
-        inner = weight.dim()
-        if inner != 1 and inner != 2:
-            raise ValueError("weight must be [d] or [H, d]")
-    shape, ldx, device = _activation(x, inner)
-    pshape = shape[-inner:]
-    w = _check("weight", weight, pshape, torch.float32, device)
-    d = shape[-1]
-    H = 1 if inner == 1 else shape[-2]
-    n = x.numel()
-    return (shape, ldx, device, (n // (H * d) if n else 0, H, d), pshape, w)
+    if stream is not None:
+        with _on(x, stream):
+            return linear_backward(
+                x, log_alpha, initial_state, d_out, d_final_state,
+                chunk_states=chunk_states, gate=gate, cu_seqlens=cu_seqlens,
+                need_initial_state_grad=need_initial_state_grad)
+    r = (_native or _load_native()).linear_backward(
+        x, log_alpha, initial_state, d_out, d_final_state, chunk_states, gate,
+        cu_seqlens, need_initial_state_grad)
+    if r.__class__ is int:
+        raise GdrError(r, "gdr_linear_backward")
+    return r
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
@@ -873,22 +708,13 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
     None), or x [.., H, d] with parameters [H, d], one row of them per head.
     A bias needs a weight.  Tokens of x may be evenly spaced columns of a
     wider tensor."""
-    lib = load_library()
-    if bias is not None and weight is None:
-        raise ValueError("a bias needs a weight")
-    shape, ldx, device, sizes, pshape, w = _norm_args(x, weight)
-    b = _check("bias", bias, pshape, torch.float32, device)
-    _check("out", out, shape, x.dtype, device)
-
-    def call(handle):
-        o = out if out is not None else _like(x)
-        rc = lib.gdr_layer_norm(x.data_ptr(), ldx, w, b, o.data_ptr(), *sizes,
-                                eps, DTYPES[x.dtype], handle)
-        if rc != 0:
-            raise GdrError(rc, "gdr_layer_norm")
-        return o
-
-    return _launch(device, stream, call)
+    if stream is not None:
+        with _on(x, stream):
+            return layer_norm(x, weight, bias, eps=eps, out=out)
+    r = (_native or _load_native()).layer_norm(x, weight, bias, eps, out)
+    if r.__class__ is int:
+        raise GdrError(r, "gdr_layer_norm")
+    return r
 
 
 def layer_norm_backward(x, weight, d_out, *, eps: float = 1e-5,
@@ -897,27 +723,15 @@ def layer_norm_backward(x, weight, d_out, *, eps: float = 1e-5,
     weight and eps) given dL/d out (the shape and dtype of x, contiguous).
     Returns a dict of CUDA tensors dx (the dtype of x), dweight and dbias
     (fp32, the shape of weight; None without a weight or if not needed)."""
-    lib = load_library()
-    shape, ldx, device, sizes, _, w = _norm_args(x, weight)
-    dy = _check("d_out", d_out, shape, x.dtype, device)
-    if dy is None:
-        raise ValueError("d_out must be given")
-
-    def call(handle):
-        dx = _like(x)
-        dw = db = None
-        if need_param_grads and weight is not None:
-            dw, db = torch.empty_like(weight), torch.empty_like(weight)
-        rc = lib.gdr_layer_norm_backward(
-            x.data_ptr(), ldx, w, dy, dx.data_ptr(),
-            None if dw is None else dw.data_ptr(),
-            None if db is None else db.data_ptr(), *sizes, eps,
-            DTYPES[x.dtype], handle)
-        if rc != 0:
-            raise GdrError(rc, "gdr_layer_norm_backward")
-        return dict(dx=dx, dweight=dw, dbias=db)
-
-    return _launch(device, stream, call)
+    if stream is not None:
+        with _on(x, stream):
+            return layer_norm_backward(x, weight, d_out, eps=eps,
+                                       need_param_grads=need_param_grads)
+    r = (_native or _load_native()).layer_norm_backward(
+        x, weight, d_out, eps, need_param_grads)
+    if r.__class__ is int:
+        raise GdrError(r, "gdr_layer_norm_backward")
+    return r
 
 
 def device_error(stream=None, clear: bool = True) -> int:

@@ -1,4 +1,5 @@
-"""Compiles libgdr (chunkwise_recurrence_b200/libgdr.so) for sm_100a with nvcc.
+"""Compiles libgdr (chunkwise_recurrence_b200/libgdr.so) for sm_100a with nvcc,
+and the PyTorch marshalling of some of its entries (_binding.so) with g++.
 
 Usage: python -m chunkwise_recurrence_b200.build [--force]
 The library is built in-tree so that it travels with the source tree.
@@ -16,6 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdr.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -47,8 +50,43 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_stale() -> bool:
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    deps = [BINDING_SRC, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return any(os.path.getmtime(d) > t for d in deps)
+
+
+def build_binding(force: bool = False) -> str:
+    """The CPython extension that hands PyTorch tensors to libgdr."""
+    if not force and not _binding_stale():
+        return BINDING
+    import sysconfig
+
+    import torch
+    gxx = shutil.which("g++")
+    if not gxx:
+        raise RuntimeError("g++ not found: the binding cannot be built")
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    subprocess.run(
+        [gxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+         "-I", os.path.join(root, "include"),
+         "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())),
+                            "include"),
+         BINDING_SRC, "-o", tmp, "-L", PKG, "-l:libgdr.so",
+         "-Wl,-rpath,$ORIGIN", "-L", os.path.join(root, "lib"), "-lc10",
+         "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
+        build_binding()
         return LIB
     nvcc = _nvcc()
     objdir = os.path.join(ROOT, "_build")
@@ -67,6 +105,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.run([nvcc, *NVCC_FLAGS, "-shared", *objs, "-o", tmp],
                    check=True)
     os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 
