@@ -336,29 +336,19 @@ struct Rows {
     r.set(f);
   }
   // the thread's part of a row of sums
-  __device__ __forceinline__ void sums(float *p, const Row &r,
-                                       bool add) const {
+  __device__ __forceinline__ void sums(float *p, const Row &r) const {
     float f[kE];
     r.get(f);
     if constexpr (A == kAligned) {
 #pragma unroll
       for (int e = 0; e < kE; e += 4)
-        if (has(e)) {
-          float4 *c = reinterpret_cast<float4 *>(p + column(e));
-          float4 t = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-          if (add) {
-            const float4 o = *c;
-            t = make_float4(o.x + t.x, o.y + t.y, o.z + t.z, o.w + t.w);
-          }
-          *c = t;
-        }
+        if (has(e))
+          *reinterpret_cast<float4 *>(p + column(e)) =
+              make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
     } else {
 #pragma unroll
       for (int e = 0; e < kE; ++e)
-        if (has(e)) {
-          float *c = p + column(e);
-          *c = add ? *c + f[e] : f[e];
-        }
+        if (has(e)) p[column(e)] = f[e];
     }
   }
 };
@@ -422,9 +412,12 @@ template <typename T, int A, int G>
 __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kBwdBlocks)
     gdr_norm_bwd_kernel(const T *x, long long ldx, const float *w,
                         const T *dy, T *dx, float *part_w, float *part_b,
-                        int ntok, int H, int d, float eps) {
+                        bool direct, int ntok, int H, int d, float eps) {
   using RW = Rows<T, A, G, 2>;
   constexpr int B = block_of(G);
+  // (the second kernel may take its places on the SMs as they get free; it
+  // waits there for the end of this one)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(128) char slots[];
   __shared__ float2 sm[2][B / 32];
   const Share q = share<G>(H);
@@ -486,41 +479,74 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kBwdBlock
   // the block's sums meet in shared memory (its groups of one head in order),
   // then those of the cluster's blocks, each block a part of the columns
   if (!part_w && !part_b) return;
-  if (gridDim.x > 8 && q.K == 1) {      // (alone, and nothing to add)
-    const long long o = blockIdx.x * ldo + pc;
-    if (part_w) rows.sums(part_w + o, aw, false);
-    if (part_b) rows.sums(part_b + o, ab, false);
+  if (direct) {                         // a partial row per group
+    if (!q.active) return;
+    const long long o = ((long long)blockIdx.x * q.K + q.kk) * ldo + pc;
+    if (part_w) rows.sums(part_w + o, aw);
+    if (part_b) rows.sums(part_b + o, ab);
     return;
   }
   copies_landed();
   __syncthreads();
-  float *cs = reinterpret_cast<float *>(slots);     // [2][B * kE]
-  const int HB = min(H, B / G), h0 = blockIdx.y * HB;
-  for (int k = 0; k < q.K; ++k) {
-    if (q.kk == k) {
-      float *at = cs + (q.head - h0) * d;
-      rows.sums(at, aw, k > 0);
-      rows.sums(at + B * kE, ab, k > 0);
-    }
-    __syncthreads();
+  constexpr int GE = G * kE;                        // room for a group's row
+  float *cs = reinterpret_cast<float *>(slots);     // [2][B / G][GE]
+  if (q.active) {
+    float *mine = cs + threadIdx.x / G * GE;
+    rows.sums(mine, aw);
+    rows.sums(mine + B * kE, ab);
   }
   cg::cluster_group cl = cg::this_cluster();
   const int nc = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  if (nc > 1) cl.sync();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int HB = min(H, B / G), h0 = blockIdx.y * HB;
   const int cols = min(HB, H - h0) * d;
-  const long long o = (long long)(blockIdx.x / nc) * H * d + (long long)h0 * d;
+  const long long o = (long long)(blockIdx.x / nc) * ldo + (long long)h0 * d;
+  __syncthreads();
+  constexpr int V = A == kAligned ? 4 : 1;          // columns at a time
+  if (nc == 1 || q.K > 1)
+    for (int c = threadIdx.x * V; c < cols; c += B * V) {
+      const int hb = HB > 1 ? c / d : 0;
+      float *at = cs + hb * GE + (c - hb * d);
+      float sum[2][V] = {};
+#pragma unroll 4
+      for (int k = 0; k < q.K; ++k)
+#pragma unroll
+        for (int w2 = 0; w2 < 2; ++w2) {
+          float f[V];
+          const float *from = at + k * HB * GE + w2 * B * kE;
+          if constexpr (V == 4) {
+            const float4 t = *reinterpret_cast<const float4 *>(from);
+            f[0] = t.x, f[1] = t.y, f[2] = t.z, f[3] = t.w;
+          } else {
+            f[0] = *from;
+          }
+#pragma unroll
+          for (int v = 0; v < V; ++v) sum[w2][v] += f[v];
+        }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (nc > 1) {            // (no other thread reads these columns here)
+          at[v] = sum[0][v];
+          at[v + B * kE] = sum[1][v];
+        } else {
+          if (part_w) part_w[o + c + v] = sum[0][v];
+          if (part_b) part_b[o + c + v] = sum[1][v];
+        }
+      }
+    }
+  if (nc == 1) return;
+  cl.sync();
   for (int c = rank * B + threadIdx.x; c < cols; c += nc * B) {
+    const int hb = HB > 1 ? c / d : 0, at = hb * GE + (c - hb * d);
     float sw = 0.f, sb = 0.f;
     for (int r = 0; r < nc; ++r) {
       const float *rs = cl.map_shared_rank(cs, r);
-      sw += rs[c];
-      sb += rs[c + B * kE];
+      sw += rs[at];
+      sb += rs[at + B * kE];
     }
     if (part_w) part_w[o + c] = sw;
     if (part_b) part_b[o + c] = sb;
   }
-  if (nc > 1) cl.sync();    // none ends while another reads its sums
+  cl.sync();                // none ends while another reads its sums
 }
 
 // dst[c] = the sum over `slices` rows of part[.][c], c < n: 32 columns a
@@ -563,6 +589,8 @@ struct NormParams {
   int access, G;           // how rows are read; threads per row
   int slices;              // blocks side by side over the tokens
   int cluster;             // of which this many add their sums
+  int parts;               // partial rows of sums
+  bool direct;             // ... one per group of threads, not per block
   int ntok, H, d;
   float eps;
 };
@@ -609,11 +637,23 @@ int slices_of(const NormParams &p, int resident) {
 void cut_bwd(NormParams *p) {
   const Cut c = cut_of(p->H, p->G);
   const int blocks = (p->ntok + c.groups - 1) / c.groups;
+  p->direct = false;
   if (blocks <= 8) {
     p->slices = p->cluster = blocks;
+    p->parts = 1;
   } else {
     p->slices = slices_of(*p, kBwdBlocks);
     p->cluster = 1;
+    // Few groups leave it all to the second kernel; more add theirs block by
+    // block first, for the second kernel's reading grows with its rows (333
+    // rows of 1001, fp32, a row of sums per group 7.4 us, per block 12.3;
+    // 8192 rows of 16 heads of 128, bf16, 1184 groups, 23.1 and 23.9; 2000
+    // unaligned rows of 1001, 1184 groups, 18.6 and 16.5; 5000 rows of 8
+    // heads of 64, 2368 groups, 14.8 and 10.7).
+    p->direct = (long long)p->slices * c.groups <=
+                    (p->access == kAligned ? 1280 : 512) ||
+                c.groups == 1;
+    p->parts = p->direct ? p->slices * c.groups : p->slices;
   }
 }
 
@@ -656,7 +696,7 @@ cudaError_t launch_bwd(const NormParams &p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k, static_cast<const T *>(p.x), p.ldx, p.w,
                             static_cast<const T *>(p.dy),
                             static_cast<T *>(p.out), p.part_w, p.part_b,
-                            p.ntok, p.H, p.d, p.eps);
+                            p.direct, p.ntok, p.H, p.d, p.eps);
 }
 
 template <bool BWD, typename T, int A, int G>
@@ -811,13 +851,13 @@ extern "C" gdr_status gdr_layer_norm_backward(
   p.eps = eps;
   set_access(&p, dtype);
   cut_bwd(&p);
-  const int parts = p.slices / p.cluster;   // 1: the sums are whole
-  const size_t one = (size_t)(4 * hd * parts + 255) & ~(size_t)255;
+  // (one part: the sums are whole)
+  const size_t one = (size_t)(4 * hd * p.parts + 255) & ~(size_t)255;
   const int narr = (d_weight ? 1 : 0) + (d_bias ? 1 : 0);
   void *ws = nullptr;
   p.part_w = d_weight;
   p.part_b = d_bias;
-  if (narr && parts > 1) {
+  if (narr && p.parts > 1) {
     st = scratch_get(&ws, one * narr, stream);
     if (st != GDR_OK) return st;
     char *at = static_cast<char *>(ws);
@@ -842,7 +882,7 @@ extern "C" gdr_status gdr_layer_norm_backward(
     e = cudaLaunchKernelEx(&cfg, gdr_norm_sum_kernel,
                            static_cast<const float *>(p.part_w),
                            static_cast<const float *>(p.part_b), d_weight,
-                           d_bias, (int)hd, parts);
+                           d_bias, (int)hd, p.parts);
   }
   const cudaError_t f = ws ? scratch_put(ws, stream) : cudaSuccess;
   return (e == cudaSuccess && f == cudaSuccess) ? GDR_OK : GDR_ERR_CUDA;

@@ -719,7 +719,7 @@ GDR_API gdr_status gdr_layer_norm(const void *x, long long ldx,
  * [ntok][H][d] in `dtype`; dx the same (written); d_weight and d_bias [H][d]
  * fp32 (written, summed over the tokens in fp32 and in a fixed order), each
  * NULL to skip.  With no token dx is empty and the sums are zero.  Scratch
- * for d_weight and d_bias, but for few tokens: up to 296 rows of H d floats
+ * for d_weight and d_bias, but for few tokens: up to 1280 rows of H d floats
  * each, stream-ordered from the library's pool; GDR_ERR_OUT_OF_MEMORY on
  * failure.  A row with an infinity or NaN gives NaN in its dx and in the sums.
  */
