@@ -10,11 +10,11 @@
 //
 // One pass over the data.  A thread holds 8 tokens of 4 channels in registers
 // and scans them alone; the runs of a warp (if it has more than one) are
-// joined by shuffles, those of a CTA's eight warps in shared memory, and those
+// joined by shuffles, those of a CTA's four warps in shared memory, and those
 // of up to eight CTAs, stacked in time as a cluster, in distributed shared
 // memory.  Each thread then runs its tokens a second time from the state it
-// now knows.  Nothing but x, log_alpha and the results touches HBM, and there
-// is no scratch, flag or spin-wait.
+// now knows.  Nothing but x, log_alpha and the results touches HBM, and the
+// only waits are a cluster's, for its own CTAs.
 //
 // Decays near 1 are held as alpha - 1: rounding alpha itself to fp32 puts a
 // systematic 2^-25 into every step, which a memory of 10^4 tokens turns into
@@ -1224,12 +1224,14 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
 }
 
 // Scalar gate, heads of more than one channel tile: the tiles' shares of
-// dlog_alpha, added in order.
+// dlog_alpha, added in order; tokens outside every sequence (in order, as they
+// have to be, before the first or behind the last) have none.
 __global__ void __launch_bounds__(256)
-    gdr_linear_dla_kernel(const float *part, float *dla, long long n,
-                          int nct) {
+    gdr_linear_dla_kernel(const float *part, float *dla, long long n, int nct,
+                          const int32_t *cu, int nseq, int H) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
+  if (cu && (i < (long long)cu[0] * H || i >= (long long)cu[nseq] * H)) return;
   float s = 0.f;
   for (int c = 0; c < nct; ++c) s += part[c * n + i];
   dla[i] = s;
@@ -1660,7 +1662,7 @@ extern "C" gdr_status gdr_linear_backward(
   if (e == cudaSuccess && parts && p.ntok > 0) {
     const long long nh = (long long)p.ntok * H;   // (within memory: < 2^39)
     gdr_linear_dla_kernel<<<(unsigned)((nh + 255) / 256), 256, 0, stream>>>(
-        p.part, d_log_alpha, nh, p.nct);
+        p.part, d_log_alpha, nh, p.nct, p.cu, p.nseq, H);
     e = cudaGetLastError();
   }
   const cudaError_t f = ws ? scratch_put(ws, stream) : cudaSuccess;

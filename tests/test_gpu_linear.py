@@ -14,6 +14,8 @@ terms add 32 u |s| e^s <= 12 u.  Together
 and half a step of the output's type.  The same holds for G backwards.  A
 product G alpha h adds the two errors and its own rounding; a sum over d
 channels up to d u of the sum of magnitudes."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -203,6 +205,36 @@ def test_rows_outside_the_sequences_are_left_as_they_were():
         ref, rf, _ = oracle.linear_fwd(f64(x), f64(la), f64(s0), cu)
         assert np.allclose(f64(out)[0, 4:90], ref[0, 4:90], atol=1e-4)
         assert np.allclose(f64(fin), rf, atol=1e-4)
+
+
+@pytest.mark.parametrize("gate", ["none", "scalar", "channel"])
+@pytest.mark.parametrize("d", [20, 100])
+def test_gradients_outside_the_sequences_are_left_as_they_were(gate, d):
+    """Through the C ABI, into buffers that already hold something."""
+    cu, T, H = [4, 40, 40, 90], 130, 2
+    x, la, s0, dO, dS = inputs(1, T, H, d, "fp32", gate, cu=cu)
+    dx = torch.full_like(x, 7.0)
+    dla = None if la is None else torch.full_like(la, 7.0)
+    ds0 = torch.empty_like(s0)
+    cut = cu_tensor(cu)
+    opts = gdr._Opts(dtype=gdr.DTYPES[torch.float32], gate=gdr.GATES[gate],
+                     cu_seqlens=cut.data_ptr(), num_seqs=len(cu) - 1,
+                     algo=gdr.ALGOS["auto"])
+    fp = ctypes.POINTER(ctypes.c_float)
+    f = lambda t: None if t is None else ctypes.cast(t.data_ptr(), fp)  # noqa: E731
+    rc = gdr.load_library().gdr_linear_backward(
+        x.data_ptr(), H * d, f(la), f(s0), None, dO.data_ptr(), f(dS),
+        dx.data_ptr(), f(dla), f(ds0), 1, T, H, d,
+        torch.cuda.current_stream().cuda_stream, ctypes.byref(opts))
+    assert rc == 0
+    torch.cuda.synchronize()
+    for t in (dx, dla):
+        if t is not None:
+            assert (t[0, :4] == 7).all() and (t[0, 90:] == 7).all()
+            t[0, :4] = 0
+            t[0, 90:] = 0
+    check_bwd(x, la, s0, dO, dS, dict(dx=dx, dlog_alpha=dla,
+                                      dinitial_state=ds0), cu)
 
 
 def test_many_short_sequences():
