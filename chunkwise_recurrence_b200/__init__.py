@@ -639,7 +639,8 @@ def linear_fwd(x, log_alpha=None, initial_state=None, *,
     gate) or None, fp32; initial_state [N, H, d] fp32 or None (zero), N = B or
     the number of packed sequences.  Returns (out, final_state), or (out,
     final_state, chunk_states) with ``output_chunk_states``: pass the latter
-    to ``linear_backward``.  final_state is None if not requested.
+    to ``linear_backward``.  final_state is None if not requested.  Rows
+    outside every packed sequence are not written.
     """
     if stream is not None:
         with _on(x, stream):
@@ -686,7 +687,8 @@ def linear_backward(x, log_alpha, initial_state, d_out, d_final_state=None, *,
     optionally, dL/d final_state.  ``chunk_states`` as ``linear_fwd`` returned
     it for these inputs, or None (computed again).  Returns a dict of CUDA
     tensors dx (the dtype of x), dlog_alpha (fp32; None without a gate) and
-    dinitial_state (fp32; None unless requested)."""
+    dinitial_state (fp32; None unless requested); rows outside every packed
+    sequence are not written."""
     if stream is not None:
         with _on(x, stream):
             return linear_backward(

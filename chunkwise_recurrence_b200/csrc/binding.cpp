@@ -248,6 +248,18 @@ Sequences sequences(PyObject *xo, PyObject *la, PyObject *s0, PyObject *gate,
   return s;
 }
 
+// Without the interpreter's lock while it lives: a launch may wait for room in
+// the driver's queue, and what empties the queue may be another Python thread.
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F>
+int call(F &&f) {
+  const Unlocked u;
+  return f();
+}
+
 template <typename F>
 PyObject *guarded(Py_ssize_t have, Py_ssize_t want, F &&f) {
   HANDLE_TH_ERRORS
@@ -279,10 +291,12 @@ PyObject *linear_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     else if (want_f)
       fin.set(floats(s.states, s.x));
     if (want_c) cs.set(floats(s.chunks, s.x));
-    const int rc = gdr_linear_fwd(
-        s.x.t->data_ptr(), s.x.ld, s.g.la, s.s0, out.p,
-        static_cast<float *>(fin.p), static_cast<float *>(cs.p), s.B, s.T,
-        s.H, s.d, stream_of(s.x), &s.g.opts);
+    const int rc = call([&] {
+      return gdr_linear_fwd(s.x.t->data_ptr(), s.x.ld, s.g.la, s.s0, out.p,
+                            static_cast<float *>(fin.p),
+                            static_cast<float *>(cs.p), s.B, s.T, s.H, s.d,
+                            stream_of(s.x), &s.g.opts);
+    });
     if (rc != GDR_OK) return PyLong_FromLong(rc);
     return want_c ? tuple({&out, &fin, &cs}) : tuple({&out, &fin});
   });
@@ -294,6 +308,8 @@ PyObject *linear_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (tensor("x", a[0]).dim() != 3)
       refuse("x must be [N, H, d]");
     const Input x = input(a[0], 2);
+    const int N = size_of(x.shape[0]), H = size_of(x.shape[1]);
+    const int d = size_of(x.shape[2]);
     const Gate g = gate_of(a[5], a[1], x);
     void *s = check("state", a[2], x.shape, at::kFloat, x);
     void *o = check_like("out", a[3], x);
@@ -307,10 +323,12 @@ PyObject *linear_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
       state.set(a[2], s);
     else
       state.set(floats(x.shape, x));
-    const int rc = gdr_linear_step(
-        x.t->data_ptr(), x.ld, g.la, static_cast<float *>(s),
-        static_cast<float *>(state.p), out.p, size_of(x.shape[0]),
-        size_of(x.shape[1]), size_of(x.shape[2]), stream_of(x), &g.opts);
+    const int rc = call([&] {
+      return gdr_linear_step(x.t->data_ptr(), x.ld, g.la,
+                             static_cast<float *>(s),
+                             static_cast<float *>(state.p), out.p, N, H, d,
+                             stream_of(x), &g.opts);
+    });
     if (rc != GDR_OK) return PyLong_FromLong(rc);
     return tuple({&out, &state});
   });
@@ -331,11 +349,13 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     dx.set(like(s.x));
     if (given(a[1])) dla.set(at::empty_like(THPVariable_Unpack(a[1])));
     if (want) ds0.set(floats(s.states, s.x));
-    const int rc = gdr_linear_backward(
-        s.x.t->data_ptr(), s.x.ld, s.g.la, s.s0, static_cast<float *>(cs),
-        dout, static_cast<float *>(ds), dx.p, static_cast<float *>(dla.p),
-        static_cast<float *>(ds0.p), s.B, s.T, s.H, s.d, stream_of(s.x),
-        &s.g.opts);
+    const int rc = call([&] {
+      return gdr_linear_backward(
+          s.x.t->data_ptr(), s.x.ld, s.g.la, s.s0, static_cast<float *>(cs),
+          dout, static_cast<float *>(ds), dx.p, static_cast<float *>(dla.p),
+          static_cast<float *>(ds0.p), s.B, s.T, s.H, s.d, stream_of(s.x),
+          &s.g.opts);
+    });
     if (rc != GDR_OK) return PyLong_FromLong(rc);
     return dict({{"dx", &dx},
                  {"dlog_alpha", &dla},
@@ -385,9 +405,11 @@ PyObject *layer_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard guard(r.x.device);
     Result out;
     given(a[4]) ? out.set(a[4], o) : out.set(like(r.x));
-    const int rc = gdr_layer_norm(r.x.t->data_ptr(), r.x.ld, r.w,
-                                  static_cast<float *>(b), out.p, r.ntok, r.H,
-                                  r.d, eps, r.x.dtype, stream_of(r.x));
+    const int rc = call([&] {
+      return gdr_layer_norm(r.x.t->data_ptr(), r.x.ld, r.w,
+                            static_cast<float *>(b), out.p, r.ntok, r.H, r.d,
+                            eps, r.x.dtype, stream_of(r.x));
+    });
     if (rc != GDR_OK) return PyLong_FromLong(rc);
     Py_INCREF(out.o);
     return out.o;
@@ -409,10 +431,12 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
       dw.set(floats(r.params, r.x));
       db.set(floats(r.params, r.x));
     }
-    const int rc = gdr_layer_norm_backward(
-        r.x.t->data_ptr(), r.x.ld, r.w, dy, dx.p, static_cast<float *>(dw.p),
-        static_cast<float *>(db.p), r.ntok, r.H, r.d, eps, r.x.dtype,
-        stream_of(r.x));
+    const int rc = call([&] {
+      return gdr_layer_norm_backward(
+          r.x.t->data_ptr(), r.x.ld, r.w, dy, dx.p,
+          static_cast<float *>(dw.p), static_cast<float *>(db.p), r.ntok, r.H,
+          r.d, eps, r.x.dtype, stream_of(r.x));
+    });
     if (rc != GDR_OK) return PyLong_FromLong(rc);
     return dict({{"dx", &dx}, {"dweight", &dw}, {"dbias", &db}});
   });

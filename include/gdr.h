@@ -619,6 +619,10 @@ GDR_API gdr_status gdr_efla_beta_backward(const void *k, const float *beta,
  * non-decreasing within [0, T]; rows of out outside every sequence are left
  * as they were.  Buffers that are written must not overlap any other.
  *
+ * NaN stays in its sequence and channel; an infinity in x or in a state is
+ * NaN one token on (decays near 1 are applied as h + (alpha - 1) h), and so
+ * may be a state after decays > 1 whose product alone is beyond fp32.
+ *
  * Sizes: B, T, H >= 0, d >= 1, H <= 65535, H d <= 2^24; at most 2^28
  * (sequence, 32-channel) pairs.  State and sums are fp32; out is rounded
  * once.  ldx < 2^30.  opts->algo must be AUTO.  One launch, no scratch;
