@@ -262,11 +262,21 @@ __device__ __forceinline__ void factors(float (&m)[GV], float (&sum)[GV]) {
   }
 }
 
-// the map (s, b): y -> e^s y + b
-template <int GATE, bool TIGHT = false>
+// The factor (any form) of one decay after another: where both are held as
+// alpha - 1 so is the product, unless it is far from 1.
+__device__ __forceinline__ float compose(float a, float b) {
+  const float m = fmaf(a, b, a + b);
+  const float p = decay<false>(a, 1.f) * decay<false>(b, 1.f);
+  return (__float_as_int(a) & __float_as_int(b)) < 0 && m > -0.5f ? -fabsf(m)
+                                                                  : p;
+}
+// the factor that changes nothing, in both forms
+constexpr float kNoDecay = -0.f;
+
+// the map (factor in any form, b): y -> e^s y + b
+template <int GATE>
 __device__ __forceinline__ float apply(float2 m, float y) {
-  if constexpr (GATE == GDR_GATE_NONE) return y + m.y;
-  return decay<TIGHT>(decay_factor<TIGHT>(m.x), y) + m.y;
+  return decayed<GATE, false>(m.x, y) + m.y;
 }
 
 template <bool B>
@@ -321,8 +331,28 @@ struct Tile {
 
 template <int GV>
 struct Map {       // y -> e^s y + b per channel of a thread
-  float s[GV], b[kV];
+  float s[GV], b[kV];   // s: the sum of log-decays, then the factor
 };
+// From the sums to the factors.
+template <int GV, int GATE>
+__device__ __forceinline__ void to_factors(Map<GV> &f, bool tight) {
+  if constexpr (GATE == GDR_GATE_NONE) return;
+  if (!tight) {
+#pragma unroll
+    for (int v = 0; v < GV; ++v) f.s[v] = decay_factor<false>(f.s[v]);
+  } else if constexpr (GV == kV) {
+#pragma unroll
+    for (int v = 0; v < GV; v += 2)
+      split(expm1_tight(pair(f.s[v], f.s[v + 1])), f.s[v], f.s[v + 1]);
+  } else {
+    f.s[0] = expm1_tight(f.s[0]);
+  }
+}
+// y <- the map at y
+template <int GV, int GATE, bool TIGHT>
+__device__ __forceinline__ void apply_all(float (&y)[kV], const Map<GV> &f) {
+  advance<GV, GATE, TIGHT>(y, f.s, f.b);
+}
 
 // Scan of the warp's runs, in time (REV = false) or against it: on return
 // `f` maps over this run and all before it (in scan order), `ex` over those
@@ -337,31 +367,45 @@ __device__ __forceinline__ void warp_scan(Map<GV> &f, Map<GV> &ex,
     };
     auto stage = [&](int off, auto tc) {
       const bool has = REV ? lane + off < 32 : lane >= off;
+      float y[kV];
 #pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        const float gb = from(f.b[v], off);
-        const float y = apply<GATE, tc.value>(
-            make_float2(f.s[GV == kV ? v : 0], f.b[v]), gb);
-        if (has) f.b[v] = y;
-      }
+      for (int v = 0; v < kV; ++v) y[v] = from(f.b[v], off);
+      apply_all<GV, GATE, tc.value>(y, f);
 #pragma unroll
-      for (int v = 0; v < GV; ++v) {
-        const float gs = from(f.s[v], off);
-        if (has) f.s[v] += gs;
+      for (int v = 0; v < kV; ++v)
+        if (has) f.b[v] = y[v];
+      if constexpr (GATE != GDR_GATE_NONE) {
+#pragma unroll
+        for (int v = 0; v < GV; ++v) {
+          const float g = from(f.s[v], off);
+          const float m = tc.value ? fmaf(f.s[v], g, f.s[v] + g)
+                                   : compose(f.s[v], g);
+          if (has) f.s[v] = m;
+        }
       }
     };
-    if (tight) stage(LANES, Bool<true>{}); else stage(LANES, Bool<false>{});
-    if constexpr (LANES < 16) stage(2 * LANES, Bool<false>{});
+    auto all = [&](auto tc) {
+      stage(LANES, tc);
+      if constexpr (LANES < 16) stage(2 * LANES, tc);
+    };
+    if (tight) all(Bool<true>{}); else all(Bool<false>{});
     const bool first = REV ? lane + LANES >= 32 : lane < LANES;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
       const float b = from(f.b[v], LANES);
       ex.b[v] = first ? 0.f : b;
     }
+    if constexpr (GATE != GDR_GATE_NONE) {
 #pragma unroll
-    for (int v = 0; v < GV; ++v) {
-      const float s = from(f.s[v], LANES);
-      ex.s[v] = first ? 0.f : s;
+      for (int v = 0; v < GV; ++v) {
+        const float m = from(f.s[v], LANES);
+        ex.s[v] = first ? kNoDecay : m;
+      }
+      // (from here on in any form)
+      if (tight) {
+#pragma unroll
+        for (int v = 0; v < GV; ++v) f.s[v] = -fabsf(f.s[v]);
+      }
     }
   }
 }
@@ -370,14 +414,10 @@ template <int LANES, int GV, int GATE>
 __device__ __forceinline__ void enter(float (&y)[kV], const Map<GV> &ex,
                                       bool tight) {
   if constexpr (LANES < 32) {
-    auto go = [&](auto tc) {
-#pragma unroll
-      for (int v = 0; v < kV; ++v)
-        y[v] = apply<GATE, tc.value>(
-            make_float2(ex.s[GV == kV ? v : 0], ex.b[v]), y[v]);
-    };
-    // (two runs per warp: `ex` is one run's map)
-    if (LANES == 16 && tight) go(Bool<true>{}); else go(Bool<false>{});
+    if (tight)
+      apply_all<GV, GATE, true>(y, ex);
+    else
+      apply_all<GV, GATE, false>(y, ex);
   }
 }
 
@@ -845,17 +885,21 @@ __device__ __forceinline__ void run_maps(J &jt, int step, int nc, int rank,
       // (after an expired wait nothing more is sent, expected or waited for)
       if (i == 0 && limit > 0)
         mbar_arrive_expect_tx(&jt.full[buf], nc * CH * (int)sizeof(float2));
-      float2 m = make_float2(0.f, 0.f);
+      float2 m = make_float2(kNoDecay, 0.f);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const float2 g = jt.warp[REV ? kWarps - 1 - k : k][i];
         pre[k] = m;
-        m = make_float2(m.x + g.x, apply<GATE>(g, m.y));
+        m = make_float2(compose(m.x, g.x), apply<GATE>(g, m.y));
       }
-      if (!mute && limit > 0)
-        for (int r = 0; r < nc; ++r)
-          send_map(remote(&jt.rank[buf][rank][i], r), m,
-                   remote(&jt.full[buf], r));
+      if (!mute && limit > 0) {
+        const uint32_t off = smem_u32(&jt.rank[buf][rank][i]) -
+                             smem_u32(&jt.full[buf]);
+        for (int r = 0; r < nc; ++r) {
+          const uint32_t bar = remote(&jt.full[buf], r);
+          send_map(bar + off, m, bar);
+        }
+      }
       // bounded: after one wait that expires no other is waited for, so that
       // every CTA gets to the end, where the cluster meets once more
       if (limit > 0) {
@@ -868,10 +912,12 @@ __device__ __forceinline__ void run_maps(J &jt, int step, int nc, int rank,
           }
       }
       float y = 0.f;
-      for (int r = 0; r < nc; ++r) {
-        if (r == rank) y = carry;
-        carry = apply<GATE>(jt.rank[buf][r][i], carry);
-      }
+#pragma unroll (REV ? 1 : kMaxCluster)
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < nc) {
+          if (r == rank) y = carry;
+          carry = apply<GATE>(jt.rank[buf][r][i], carry);
+        }
 #pragma unroll
       for (int k = 0; k < kWarps; ++k)
         jt.in[REV ? kWarps - 1 - k : k][i] = apply<GATE>(pre[k], y);
@@ -981,6 +1027,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     };
     if (tight) alone(Bool<true>{}); else alone(Bool<false>{});
     const bool runs = is_tight_run<GV, GATE>(f.s, tight);
+    to_factors<GV, GATE>(f, runs);
     warp_scan<LANES, GV, GATE, false>(f, ex, runs);
     // what enters the warp's tile
     float h[kV];
@@ -1150,6 +1197,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     if (tight) both(Bool<true>{}); else both(Bool<false>{});
     if (k + 1 < steps) in.fetch_x(slots, in.x, tn + off, end_at(tn));
     const bool runs = is_tight_run<GV, GATE>(f.s, tight);
+    to_factors<GV, GATE>(f, runs);
     warp_scan<LANES, GV, GATE, true>(f, ex, runs);
     float cy[kV];
     if constexpr (WPC == 1) {
