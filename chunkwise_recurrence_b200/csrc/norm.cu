@@ -105,18 +105,32 @@ __device__ __forceinline__ void store(float *p, const float *f) {
 // thread may still be reading).
 template <int G, bool TWO>
 __device__ __forceinline__ void group_sum(float &a, float &b, float2 *sm) {
-  auto fold = [&](int o) {
-    a += __shfl_xor_sync(~0u, a, o);
-    if constexpr (TWO) b += __shfl_xor_sync(~0u, b, o);
-  };
+  constexpr int W = G < 32 ? G : 32;
+  if constexpr (W > 1 && TWO) {
+    // the lower half of the threads goes on with a, the upper half with b
+    const bool up = threadIdx.x & (W / 2);
+    const float give = up ? a : b;
+    float keep = up ? b : a;
+    keep += __shfl_xor_sync(~0u, give, W / 2);
 #pragma unroll
-  for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) fold(o);
+    for (int o = W / 4; o > 0; o >>= 1) keep += __shfl_xor_sync(~0u, keep, o);
+    if constexpr (G <= 32) {
+      const float other = __shfl_xor_sync(~0u, keep, W / 2);
+      a = up ? other : keep;
+      b = up ? keep : other;
+    } else {
+      if (threadIdx.x % 16 == 0)
+        reinterpret_cast<float *>(sm)[threadIdx.x / 16] = keep;
+    }
+  } else {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
+    if (G > 32 && threadIdx.x % 32 == 0) sm[threadIdx.x / 32].x = a;
+  }
   if constexpr (G > 32) {
     constexpr int NW = G / 32;
-    const int w = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) sm[w] = make_float2(a, b);
     sm100::named_bar_sync(1 + threadIdx.x / G, G);
-    const float2 *g = sm + (w / NW) * NW;
+    const float2 *g = sm + threadIdx.x / G * NW;
     if constexpr (NW <= 8) {
       a = b = 0.f;
 #pragma unroll
@@ -126,9 +140,13 @@ __device__ __forceinline__ void group_sum(float &a, float &b, float2 *sm) {
       }
     } else {
       const float2 t = g[threadIdx.x % NW];
-      a = t.x, b = t.y;
+      a = t.x;
+      if constexpr (TWO) b = t.y;
 #pragma unroll
-      for (int o = NW / 2; o > 0; o >>= 1) fold(o);
+      for (int o = NW / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(~0u, a, o);
+        if constexpr (TWO) b += __shfl_xor_sync(~0u, b, o);
+      }
     }
   }
 }
