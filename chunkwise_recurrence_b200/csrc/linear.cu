@@ -18,28 +18,30 @@
 //
 // Decays near 1 are held as alpha - 1: rounding alpha itself to fp32 puts a
 // systematic 2^-25 into every step, which a memory of 10^4 tokens turns into
-// 3e-4.  Composed decays are sums of log_alpha until they are applied, so
-// that log_alpha = -inf clears the state exactly.
+// 3e-4.  A run's decay is made from its sum of log_alpha; runs, warps and CTAs
+// compose factors (joining sums and taking e^s anew at every join cost a
+// quarter of the instructions: 93 us for 8 x 4096 x 2048).  log_alpha = -inf
+// is a factor of exactly 0.
 //
 // Bound by HBM: forward 2 + 4 + 2 bytes a token and channel (bf16, a decay per
 // channel), backward 2 + 4 + 2 + 2 + 4 and half a byte of chunk states.  What
 // it takes to get near: inputs sent for one step ahead (cp.async into slots
-// that only their thread reads), about 23 (forward) and 38 (backward)
-// instructions a value through packed fp32 pairs, four CTAs of four warps an
-// SM so that one's joins hide behind the others' arithmetic, and no
-// cluster-wide barrier.  Measured (us, share of the 6.53 TB/s a copy reaches;
-// batch x tokens x channels, decay per channel, bf16 unless said):
-//   forward  8 x 4096 x 2048  93 (0.89); fp32 4 x 4096 x 2048 76 (0.81);
-//            64 x 512 x 2048 87 (0.94); 1 x 65536 x 2048 236 (0.70)
-//   backward 8 x 4096 x 2048 169 (1.0); fp32 4 x 4096 x 2048 129 (0.98);
-//            1 x 65536 x 2048 392 (0.86)
+// that only their thread reads), 19 (forward) and 35 (backward) instructions
+// a value through packed fp32 pairs, four CTAs of four warps an SM so that
+// one's joins hide behind the others' arithmetic, and no cluster-wide barrier.
+// Measured (us, share of the 6.53 TB/s a copy reaches; batch x tokens x
+// channels, decay per channel, bf16 unless said):
+//   forward  8 x 4096 x 2048  85 (0.97); fp32 4 x 4096 x 2048 73 (0.84);
+//            64 x 512 x 2048 84 (0.98); 1 x 65536 x 2048 201 (0.82)
+//   backward 8 x 4096 x 2048 163 (0.91); fp32 4 x 4096 x 2048 121 (0.87);
+//            1 x 65536 x 2048 350 (0.85)
 // One long sequence is 64 chains cut over 8 CTAs each; every step of 1024
 // tokens then waits for the slowest of the eight and for the exchange, about
-// 0.7 us of 3.6.  Longer runs of the forward pass draw the full 1000 W and
-// the clock falls to 1.78 GHz (8 x 4096 x 2048: 100 us).  A decay per head
-// leaves half the bytes and the same arithmetic: 66 us of 41 forward, 115 of
-// 67 backward.  Rows that are not aligned (H d odd) take 37 to 63
-// instructions a value: 8 x 2000 x 3030 143 us (0.41).
+// 0.5 us of 3.1.  Longer runs of the forward pass draw the full 1000 W and
+// the clock falls to 1.78 GHz (8 x 4096 x 2048: 96 us).  A decay per head
+// leaves half the bytes and most of the arithmetic: 65 us of 42 forward, 114
+// of 68 backward.  Rows that are not aligned (H d odd) take twice the
+// instructions: 8 x 2000 x 3030 130 us (0.46).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -964,6 +966,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     gdr_linear_fwd_kernel(const LinParams p) {
   using TL = Tile<LANES, GATE>;
   constexpr int GV = TL::GV, CH = TL::kCh;
+  prior_done();
+  next_may_start();
   using IN = Inputs<T, VEC, GATE, false>;
   using raw_t = typename IN::raw_t;
   extern __shared__ __align__(128) char slots[];
@@ -1115,6 +1119,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     gdr_linear_bwd_kernel(const LinParams p) {
   using TL = Tile<LANES, GATE>;
   constexpr int GV = TL::GV, CH = TL::kCh;
+  prior_done();
+  next_may_start();
   using IN = Inputs<T, VEC, GATE, true>;
   using raw_t = typename IN::raw_t;
   extern __shared__ __align__(128) char slots[];
@@ -1277,6 +1283,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
 __global__ void __launch_bounds__(256)
     gdr_linear_dla_kernel(const float *part, float *dla, long long n, int nct,
                           const int32_t *cu, int nseq, int H) {
+  prior_done();
+  next_may_start();
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   if (cu && (i < (long long)cu[0] * H || i >= (long long)cu[nseq] * H)) return;
@@ -1300,6 +1308,8 @@ __global__ void __launch_bounds__(128)
                            int d) {
   constexpr int V = VEC ? kV : 1;
   const int D = H * d, nv = D / V;
+  prior_done();
+  next_may_start();
   const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
   if (i >= (long long)N * nv) return;
   const long long n = i / nv;
@@ -1348,6 +1358,7 @@ struct Plan {
   bool vec;        // rows are aligned for vectors of four channels
   int lanes, wpc;  // a warp's tile is 4 lanes channels wide; warps per chain
   int nc;          // CTAs per chain
+  bool early;      // see launch()
 };
 
 constexpr int kSms = 148;
@@ -1375,8 +1386,8 @@ gdr_status plan(Op op, const gdr_opts &o, LinParams *p, Plan *pl) {
   };
   // Sequences too short for a CTA's tile are run by single warps.  So are, in
   // the forward pass, those up to half as long again, if they alone fill the
-  // GPU (bf16, 2048 channels, 33.5 M tokens x channels: 96 tokens 97 us
-  // against 136, 192 tokens 100 against 124, 256 tokens 101 against 92).
+  // GPU (32768 tokens of 2048 channels, bf16: 96 tokens each 91 us against
+  // 121, 192 tokens 95 against 101, 256 tokens 96 against 84).
   long long chains = cut(8);
   const bool short_seqs =
       2 * avg <= btok || (!bwd && pl->vec && 2 * avg <= 3 * btok &&
@@ -1388,14 +1399,20 @@ gdr_status plan(Op op, const gdr_opts &o, LinParams *p, Plan *pl) {
   // CTAs per chain: the more, the more of a long sequence is under way at
   // once, but a step then waits for all of them.  Best as long as the launch
   // stays about this big (forward, bf16, 512 chains of 4096 tokens: 1 CTA
-  // 93 us, 8 CTAs 126; 64 chains of 65536: 1 CTA 720 us, 8 CTAs 228;
-  // backward, 256 chains of 4096: 1 CTA 167, 2 205, 8 169).
+  // 85 us, 8 CTAs 113; 64 chains of 65536: 1 CTA 557 us, 8 CTAs 201;
+  // backward, 256 chains of 4096: 1 CTA 170, 2 210, 8 164).
   const int ctas = bwd ? (bf16 ? 2048 : 1024) : bf16 ? 4 * kSms : 2048;
   pl->nc = 1;
   if (pl->wpc > 1)
     while (pl->nc < kMaxCluster && pl->nc * btok < avg &&
            chains * pl->nc * 2 <= ctas)
       pl->nc *= 2;
+  // Blocks that take their places while the launch before ends start sooner,
+  // but are not spread evenly, which long ones feel (2048 channels, bf16, us a
+  // call without and with: forward 8 x 512 tokens 16.7 and 13.8, 8 x 1024 25.4
+  // and 23.7, 8 x 4096 84.6 and 88.3; backward 8 x 512 33.6 and 32.4,
+  // 1 x 8192 49.7 and 53.8, 1 x 65536 350 and 393).
+  pl->early = avg <= 8 * pl->nc * btok;
   return GDR_OK;
 }
 
@@ -1405,22 +1422,12 @@ cudaError_t launch_chains(K kernel, int slots, const LinParams &p,
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, slots);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(pl.wpc == 1 ? (p.chains + kWarps - 1) / kWarps
-                                 : p.chains * pl.nc);
   LinParams q = p;
   q.nc = pl.nc;
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = slots;
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = pl.nc;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = pl.nc > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, q);
+  return launch(kernel,
+                dim3(pl.wpc == 1 ? (p.chains + kWarps - 1) / kWarps
+                                 : p.chains * pl.nc),
+                kWarps * 32, slots, pl.nc, pl.early, s, q);
 }
 
 template <typename T, bool VEC, int GATE, bool WARP, bool CL>
@@ -1438,11 +1445,11 @@ template <typename T, bool VEC, int GATE>
 cudaError_t run3(Op op, const LinParams &p, const Plan &pl, cudaStream_t s) {
   if (op == kStep) {
     const long long n = (long long)p.nseq * (p.D / (VEC ? kV : 1));
-    gdr_linear_step_kernel<T, VEC, GATE>
-        <<<(unsigned)((n + 127) / 128), 128, 0, s>>>(
-            static_cast<const T *>(p.x), p.la, p.s0, p.sT,
-            static_cast<T *>(p.out), p.ldx, p.nseq, p.H, p.d);
-    return cudaGetLastError();
+    return launch(gdr_linear_step_kernel<T, VEC, GATE>,
+                  dim3((unsigned)((n + 127) / 128)), 128, 0, 1, true,
+                  s,
+                  static_cast<const T *>(p.x), p.la, p.s0, p.sT,
+                  static_cast<T *>(p.out), p.ldx, p.nseq, p.H, p.d);
   }
   return pl.wpc == 1  ? run4<T, VEC, GATE, true, false>(op, p, pl, s)
          : pl.nc == 1 ? run4<T, VEC, GATE, false, false>(op, p, pl, s)
@@ -1709,9 +1716,10 @@ extern "C" gdr_status gdr_linear_backward(
   if (e == cudaSuccess) e = run(kBwd, o, p, pl, stream);
   if (e == cudaSuccess && parts && p.ntok > 0) {
     const long long nh = (long long)p.ntok * H;   // (within memory: < 2^39)
-    gdr_linear_dla_kernel<<<(unsigned)((nh + 255) / 256), 256, 0, stream>>>(
-        p.part, d_log_alpha, nh, p.nct, p.cu, p.nseq, H);
-    e = cudaGetLastError();
+    e = streaming::launch(gdr_linear_dla_kernel,
+                          dim3((unsigned)((nh + 255) / 256)), 256, 0, 1, true,
+                          stream, p.part, d_log_alpha, nh, p.nct, p.cu,
+                          p.nseq, H);
   }
   const cudaError_t f = ws ? scratch_put(ws, stream) : cudaSuccess;
   return (e == cudaSuccess && f == cudaSuccess) ? GDR_OK : GDR_ERR_CUDA;

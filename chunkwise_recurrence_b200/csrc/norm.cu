@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kFwdBlock
                         const float *b, T *out, int ntok, int H, int d,
                         float eps) {
   using RW = Rows<T, A, G, 1>;
+  prior_done();
+  next_may_start();
   extern __shared__ __align__(128) char slots[];
   __shared__ float2 sm[2][block_of(G) / 32];
   const Share q = share<G>(H);
@@ -433,9 +435,8 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kBwdBlock
                         bool direct, int ntok, int H, int d, float eps) {
   using RW = Rows<T, A, G, 2>;
   constexpr int B = block_of(G);
-  // (the second kernel may take its places on the SMs as they get free; it
-  // waits there for the end of this one)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  prior_done();
+  next_may_start();
   extern __shared__ __align__(128) char slots[];
   __shared__ float2 sm[2][B / 32];
   const Share q = share<G>(H);
@@ -574,7 +575,8 @@ __global__ void __launch_bounds__(1024)
     gdr_norm_sum_kernel(const float *part_w, const float *part_b, float *dw,
                         float *db, int n, int slices) {
   __shared__ float sm[32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  prior_done();
+  next_may_start();
   const bool bias = blockIdx.y == 1 || !dw;
   const float *part = bias ? part_b : part_w;
   float *dst = bias ? db : dw;
@@ -684,10 +686,9 @@ cudaError_t launch_fwd(const NormParams &p, cudaStream_t s) {
         k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
   }
-  k<<<dim3(p.slices, cut_of(p.H, G).hblocks), block_of(G), bytes, s>>>(
-      static_cast<const T *>(p.x), p.ldx, p.w, p.b, static_cast<T *>(p.out),
-      p.ntok, p.H, p.d, p.eps);
-  return cudaGetLastError();
+  return launch(k, dim3(p.slices, cut_of(p.H, G).hblocks), block_of(G), bytes,
+                1, true, s, static_cast<const T *>(p.x), p.ldx, p.w, p.b,
+                static_cast<T *>(p.out), p.ntok, p.H, p.d, p.eps);
 }
 template <typename T, int A, int G>
 cudaError_t launch_bwd(const NormParams &p, cudaStream_t s) {
@@ -700,21 +701,10 @@ cudaError_t launch_bwd(const NormParams &p, cudaStream_t s) {
         k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.slices, cut_of(p.H, G).hblocks);
-  cfg.blockDim = dim3(block_of(G));
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = p.cluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k, static_cast<const T *>(p.x), p.ldx, p.w,
-                            static_cast<const T *>(p.dy),
-                            static_cast<T *>(p.out), p.part_w, p.part_b,
-                            p.direct, p.ntok, p.H, p.d, p.eps);
+  return launch(k, dim3(p.slices, cut_of(p.H, G).hblocks), block_of(G), bytes,
+                p.cluster, true, s, static_cast<const T *>(p.x), p.ldx, p.w,
+                static_cast<const T *>(p.dy), static_cast<T *>(p.out),
+                p.part_w, p.part_b, p.direct, p.ntok, p.H, p.d, p.eps);
 }
 
 template <bool BWD, typename T, int A, int G>
@@ -888,19 +878,9 @@ extern "C" gdr_status gdr_layer_norm_backward(
   cudaError_t e = run<true>(p, dtype, stream);
   if (e == cudaSuccess && ws) {
     // (its launch overlaps the end of the first kernel)
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((hd + 31) / 32), narr);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gdr_norm_sum_kernel,
-                           static_cast<const float *>(p.part_w),
-                           static_cast<const float *>(p.part_b), d_weight,
-                           d_bias, (int)hd, p.parts);
+    e = launch(gdr_norm_sum_kernel, dim3((unsigned)((hd + 31) / 32), narr),
+               1024, 0, 1, true, stream, p.part_w, p.part_b, d_weight, d_bias,
+               (int)hd, p.parts);
   }
   const cudaError_t f = ws ? scratch_put(ws, stream) : cudaSuccess;
   return (e == cudaSuccess && f == cudaSuccess) ? GDR_OK : GDR_ERR_CUDA;

@@ -1,14 +1,47 @@
 // streaming.cuh -- what the bandwidth-bound kernels (linear recurrence, layer
 // normalisation) share: asynchronous copies into shared memory and arithmetic
-// on pairs of fp32 values.
+// on pairs of fp32 values, and their launches.
 #pragma once
 
 #include <cstdint>
 
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 
 namespace gdr {
 namespace streaming {
+
+// Launches overlap: the blocks of the next launch, if it is `early`, may take
+// their places on the SMs as this one's last blocks leave (next_may_start,
+// once all of this one's have begun) and wait there until it has ended and its
+// results are visible (prior_done, before anything is read or written).  Layer
+// norm one call after another, bf16: backward 8192 x 16 heads of 128 25.1 us a
+// call without, 22.0 with; 32768 x 2048 72.4 and 69.4; forward 15.0 and 13.8,
+// 45.8 and 45.0.
+__device__ __forceinline__ void prior_done() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void next_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem,
+                   int cluster, bool early, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = early;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
