@@ -1398,21 +1398,41 @@ gdr_status plan(Op op, const gdr_opts &o, LinParams *p, Plan *pl) {
   p->chains = (int)chains;
   // CTAs per chain: the more, the more of a long sequence is under way at
   // once, but a step then waits for all of them.  Best as long as the launch
-  // stays about this big (forward, bf16, 512 chains of 4096 tokens: 1 CTA
-  // 85 us, 8 CTAs 113; 64 chains of 65536: 1 CTA 557 us, 8 CTAs 201;
-  // backward, 256 chains of 4096: 1 CTA 170, 2 210, 8 164).
-  const int ctas = bwd ? (bf16 ? 2048 : 1024) : bf16 ? 4 * kSms : 2048;
+  // stays about this big, in CTAs per SM (of which four fit, six without a
+  // decay): forward, bf16, 512 chains of 4096 tokens: 1 CTA 85 us, 8 CTAs 113;
+  // 64 chains of 65536: 1 CTA 557 us, 8 CTAs 201; backward, a decay per
+  // channel, bf16, 256 chains of 4096: 1 CTA 170, 8 164; a decay per head, 512
+  // chains of 2048: 1 CTA 92, 2 101, 8 119.  fp32 gains from more as long as
+  // each still has eight steps (forward, a decay per channel, 512 chains of
+  // 4096: 1 CTA 148, 4 131; of 1024: 1 CTA 38, 4 41).  Where the decays are
+  // most of the traffic, and of fp32, a launch a little larger than what fits
+  // loses to a smaller one, its last blocks running almost alone (backward,
+  // fp32, 160 chains of 16384: 4 CTAs 371, 2 334).
+  const bool channel = o.gate == GDR_GATE_CHANNEL;
+  const int few = o.gate == GDR_GATE_NONE ? 6
+                  : !bwd                  ? (channel && !bf16 ? 3 : 4)
+                  : channel               ? (bf16 ? 14 : 7)
+                                          : (bf16 ? 6 : 4);
+  const int many = bf16 ? few : bwd ? 7 : 14;
   pl->nc = 1;
   if (pl->wpc > 1)
     while (pl->nc < kMaxCluster && pl->nc * btok < avg &&
-           chains * pl->nc * 2 <= ctas)
+           chains * pl->nc * 2 <=
+               (16 * pl->nc * btok <= avg ? many : few) * kSms)
       pl->nc *= 2;
+  if (bwd && (channel || !bf16) && pl->nc > 1 && chains * pl->nc > 4 * kSms &&
+      2 * chains * pl->nc <= 11 * kSms)
+    pl->nc /= 2;
   // Blocks that take their places while the launch before ends start sooner,
-  // but are not spread evenly, which long ones feel (2048 channels, bf16, us a
-  // call without and with: forward 8 x 512 tokens 16.7 and 13.8, 8 x 1024 25.4
-  // and 23.7, 8 x 4096 84.6 and 88.3; backward 8 x 512 33.6 and 32.4,
-  // 1 x 8192 49.7 and 53.8, 1 x 65536 350 and 393).
-  pl->early = avg <= 8 * pl->nc * btok;
+  // but are not spread evenly, which long ones feel, and those of a launch
+  // that leaves room (2048 channels, bf16, a decay per channel, us a call
+  // without and with: forward 8 x 512 tokens 16.7 and 13.8, 8 x 1024 25.4 and
+  // 23.7, 8 x 4096 84.6 and 88.3; backward 8 x 512 33.6 and 32.4, 1 x 65536
+  // 350 and 393; both of 1 x 4000, 256 blocks of the backward pass, 45.7 and
+  // 56.4; of 2 x 1350 x 256, 128 blocks, 20.7 and 18.0).
+  const long long blocks = chains * pl->nc;
+  pl->early = avg <= 8 * pl->nc * btok &&
+              (blocks <= kSms || blocks >= 3 * kSms);
   return GDR_OK;
 }
 
