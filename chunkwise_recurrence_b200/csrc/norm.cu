@@ -18,16 +18,17 @@
 // the same channels of the same head and walks over tokens.  So w and b are
 // read once, the next two rows are on their way while one is computed
 // (asynchronous copies into shared memory), and the sums dw and db stay in
-// registers; each block writes one partial row of them and a second kernel
-// adds those, always in the same order.
+// registers; each block (or each group, where there are few) writes one partial
+// row of them and a second kernel adds those, always in the same order.
 //
 // Measured (bf16, us, and the share of the 6.53 TB/s a copy reaches):
-// forward 32768 x 2048 45.8 (0.90), 32768 x 16 heads of 128 45.7 (0.90);
-// backward 32768 x 2048 79 (0.78), 32768 x 16 x 128 74 (0.83).  What is left
-// of the backward pass: about 5 us for its ends and the second kernel, and
-// the two meetings a row, which two blocks an SM (128 registers a thread) do
-// not hide in full.  Rows of more than 8192 channels take 1024 threads of 64
-// registers, whose sums spill: 217 us for 4096 x 16384 (0.28).
+// forward 32768 x 2048 45 (0.91), 8192 x 16 heads of 128 13.8 (0.74);
+// backward 32768 x 2048 69 (0.89), 8192 x 16 x 128 22 (0.70), 16384 x 4096 87
+// (0.71).  What is left of the backward pass: about 5 us for its ends and the
+// second kernel, and the two meetings a row, which two blocks an SM (128
+// registers a thread) do not hide in full.  Rows of more than 8192 channels
+// take 1024 threads of 64 registers, whose sums spill: 203 us for 4096 x 16384
+// (0.30).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

@@ -3,13 +3,15 @@ the fp64 token loop of oracle/linear_ref.py.
 
 Tolerances, from the arithmetic (u = 2^-24).  M_t, the same recurrence run on
 |x| and |h0|, bounds every partial result.  A term of h_t is rounded at most
-four times in each join it passes (the composed log-decay, the decay, the
-multiply-add, the sum): its run (at most 32 tokens, twice), the joins inside a
-warp, a block and a cluster (at most 16) and one per 32-token tile of the
-sequence.  A decay e^s with s below -1/8 is off by up to 3 + 1.2 |s| units of
-2^-23 of e^s, which no more than 1 / (1 - e^-1/8) = 8.5 such steps in a row
-carry on: e^s (3 + 1.2 |s|) <= 3, so 2 * 3 * 8.5 u; composed log-decays of 32
-terms add 32 u |s| e^s <= 12 u.  Together
+four times in each join it passes (the composed decay, its product with the
+value, the multiply-add, the sum): its run (at most 32 tokens, twice), the
+joins inside a warp, a block and a cluster (at most 16) and one per 32-token
+tile of the sequence.  A decay e^s with s below -1/8 is off by up to 3 + 1.2
+|s| units of 2^-23 of e^s, which no more than 1 / (1 - e^-1/8) = 8.5 such
+steps in a row carry on: e^s (3 + 1.2 |s|) <= 3, so 2 * 3 * 8.5 u; the sum of
+a run's log-decays adds another 12 u at most.  (A product of decays that is
+held as alpha - 1 is off by up to 3 u of the value before it, not of itself;
+M changes little over the tokens of a tile of these inputs.)  Together
     |h - ref| <= K_T u M_t,   K_T = 4 (64 + 16 + T / 32) + 64,
 and half a step of the output's type.  The same holds for G backwards.  A
 product G alpha h adds the two errors and its own rounding; a sum over d
