@@ -196,6 +196,25 @@ def test_long_memory_keeps_the_decay_s_digits():
     assert (np.abs(got - ref[:, None]) <= kt(T) * U * ref[:, None]).all()
 
 
+@pytest.mark.parametrize("gate", ["scalar", "channel"])
+@pytest.mark.parametrize("decay", [0.01, 0.05, 0.12, 0.124, 0.126, 0.3])
+def test_a_decaying_state_keeps_its_digits(decay, gate):
+    """A state that nothing is added to, token after token.  Decays of a warp's
+    32 tokens are composed as alpha - 1, off by 3 u of the state before them:
+    3 u e^(32 decay) of the state after them, where they are at all (a run of 8
+    tokens no further down than 1 / e); the rest as elsewhere."""
+    T = 640
+    x = torch.zeros(1, T, 1, 64, device="cuda")
+    la = torch.full((1, T, 1) if gate == "scalar" else (1, T, 1, 64), -decay,
+                    device="cuda")
+    s0 = torch.ones(1, 1, 64, device="cuda")
+    out, fin = gdr.linear_fwd(x, la, s0)
+    ref = np.exp(-float(np.float32(decay)) * np.arange(1, T + 1))
+    per_tile = 3 * np.exp(32 * min(decay, 0.125))
+    tol = (kt(T) + per_tile * T / 32) * U * ref + 2.0 ** -126
+    assert (np.abs(f64(out)[0, :, 0, :] - ref[:, None]) <= tol[:, None]).all()
+
+
 def test_rows_outside_the_sequences_are_left_as_they_were():
     cu = [4, 40, 40, 90]
     T, H, d = 130, 2, 20

@@ -113,6 +113,101 @@ def test_forward_and_backward_match_oracle(shape, dtype):
     check_bwd(x, w, dy, res)
 
 
+# many tokens: persistent blocks, with the sums added per group, per block by
+# one or several groups of a head, and heads that do not fill the last block
+MANY = [(3000, 1, 24), (2500, 1, 77), (1500, 5, 101), (900, 7, 64),
+        (1200, 40, 16), (333, 1, 1001), (700, 1, 2048), (2000, 3, 40)]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", MANY)
+def test_many_tokens_match_oracle(shape, dtype):
+    x, w, b, dy = inputs(*shape, dtype, seed=3)
+    y = gdr.layer_norm(x, w, b)
+    res = gdr.layer_norm_backward(x, w, dy)
+    again = gdr.layer_norm_backward(x, w, dy)
+    torch.cuda.synchronize()
+    check_fwd(x, w, b, y)
+    check_bwd(x, w, dy, res)
+    assert all(torch.equal(res[k], again[k]) for k in res)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_wait_for_the_ones_before(captured):
+    """Launches overlap; a chain of calls that each read what the one before
+    wrote, with buffers written over and over, gives what it gives one call
+    at a time."""
+    x, w, b, dy = inputs(1200, 8, 64, "bf16")
+    la = -torch.rand(4, 300, 8, 64, device="cuda") * 0.1
+    buf = torch.empty_like(x)
+    out = torch.empty(4, 300, 8, 64, dtype=x.dtype, device="cuda")
+
+    def chain(wait):
+        got, cur = [], x
+        for i in range(6):
+            gdr.layer_norm(cur, w, b, out=buf)
+            wait()
+            _, fin = gdr.linear_fwd(buf.view(4, 300, 8, 64), la, out=out)
+            wait()
+            res = gdr.layer_norm_backward(out.view(1200, 8, 64), w, buf)
+            wait()
+            g = gdr.linear_backward(res["dx"].view(4, 300, 8, 64), la, fin,
+                                    out, fin)
+            wait()
+            cur = g["dx"].view(1200, 8, 64)
+            step, _ = gdr.linear_step(cur[:7], None, None)
+            got += [fin, res["dweight"], res["dbias"], g["dlog_alpha"],
+                    g["dinitial_state"], cur, step]
+        return got
+
+    want = chain(torch.cuda.synchronize)
+    nothing = lambda: None  # noqa: E731
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = chain(nothing)
+        for _ in range(2):
+            graph.replay()
+    else:
+        got = chain(nothing)
+    torch.cuda.synchronize()
+    assert len(got) == len(want)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_calls_wait_for_copies_and_for_other_streams():
+    """What a call reads comes from a copy on its stream, or from another
+    stream by an event, with a short call of its own just before."""
+    x, w, b, dy = inputs(4000, 16, 128, "bf16")
+    xl = x.view(1, 4000, 16, 128)
+    small = inputs(64, 16, 128, "bf16")[0]
+    want = gdr.linear_fwd(xl)[0]
+    norm = gdr.layer_norm(want.view_as(x), w, b)
+    host = torch.empty(x.shape, dtype=x.dtype, pin_memory=True)
+    host.copy_(x)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    back = torch.empty(x.shape, dtype=x.dtype, pin_memory=True)
+    dev, mid, out = (torch.empty_like(x) for _ in range(3))
+    for _ in range(10):
+        for t in (dev, mid, out):
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            gdr.layer_norm(small, w, b)
+            dev.copy_(host, non_blocking=True)
+            gdr.linear_fwd(dev.view_as(xl), out=mid.view_as(xl))
+            done = s1.record_event()
+        with torch.cuda.stream(s2):
+            gdr.layer_norm(small, w, b)
+            s2.wait_event(done)
+            gdr.layer_norm(mid, w, b, out=out)
+            back.copy_(out, non_blocking=True)
+        torch.cuda.synchronize()
+        assert torch.equal(mid, want.view_as(mid))
+        assert torch.equal(out, norm) and torch.equal(back, norm.cpu())
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_shared_parameters_and_none(dtype):
     x, w, b, dy = inputs(50, 3, 40, dtype)
