@@ -501,3 +501,28 @@ def test_an_expired_wait_is_reported(monkeypatch):
     out, fin = gdr.linear_fwd(x, la, s0)
     assert gdr.device_error() == 0
     check_fwd(x, la, s0, out, fin)
+
+
+@pytest.mark.parametrize("d", [128, 127])
+def test_more_values_than_32_bits_can_count(d):
+    """The last tokens of 2^31 values and more, forward and backward, against
+    the same tokens on their own."""
+    H, T, last = 16, (2 ** 31 + 2 ** 23) // (16 * d), 700
+    x = torch.zeros(1, T, H, d, dtype=torch.bfloat16, device="cuda")
+    la = torch.full((1, T, H), -0.05, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x[:, -last:] = torch.randn(last, H, d, generator=g, device="cuda").to(x)
+    out, fin = gdr.linear_fwd(x, la)
+    tail, latail = x[:, -last:].contiguous(), la[:, -last:].contiguous()
+    check_fwd(tail, latail, None, out[:, -last:], fin)
+    del out
+    res = gdr.linear_backward(x, la, None, x, fin)
+    torch.cuda.synchronize()
+    check_bwd(tail, latail, torch.zeros_like(fin), tail, fin,
+              dict(dx=res["dx"][:, -last:], dinitial_state=None,
+                   dlog_alpha=res["dlog_alpha"][:, -last:]))
+    # far before the last tokens nothing is left of anything
+    assert res["dx"][:, :T // 2].abs().max() <= 2.0 ** -126
+    assert res["dinitial_state"].abs().max() <= 2.0 ** -126
+    del x, res
+    torch.cuda.empty_cache()

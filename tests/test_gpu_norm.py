@@ -389,3 +389,27 @@ def test_a_block_of_norm_recurrence_and_head_norm(packed):
     for i, (a, b) in enumerate(pairs):
         a = f64(a).reshape(b.shape)
         assert np.abs(a - b).max() <= 1e-4 * np.abs(b).max(), i
+
+
+@pytest.mark.parametrize("d", [2048, 2047])
+def test_more_values_than_32_bits_can_count(d):
+    """The last rows of 2^31 values and more against the same rows on their
+    own."""
+    n, last = (2 ** 31 + 2 ** 23) // d, 300
+    x = torch.zeros(n, d, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x[-last:] = torch.randn(last, d, generator=g, device="cuda").to(x)
+    w, b = (torch.randn(d, generator=g, device="cuda") for _ in range(2))
+    tail = x[-last:].clone()
+    y = gdr.layer_norm(x, w, b)
+    check_fwd(tail.unsqueeze(1), w.unsqueeze(0), b.unsqueeze(0),
+              y[-last:].unsqueeze(1))
+    del y
+    # (rows of zeros have no distances, and a gradient of zeros)
+    res = gdr.layer_norm_backward(x, w, x)
+    torch.cuda.synchronize()
+    check_bwd(tail.unsqueeze(1), w.unsqueeze(0), tail.unsqueeze(1),
+              dict(dx=res["dx"][-last:].unsqueeze(1), dweight=res["dweight"],
+                   dbias=res["dbias"]))
+    del x, res
+    torch.cuda.empty_cache()
