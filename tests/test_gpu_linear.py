@@ -17,6 +17,7 @@ and half a step of the output's type.  The same holds for G backwards.  A
 product G alpha h adds the two errors and its own rounding; a sum over d
 channels up to d u of the sum of magnitudes."""
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -526,3 +527,25 @@ def test_more_values_than_32_bits_can_count(d):
     assert res["dinitial_state"].abs().max() <= 2.0 ** -126
     del x, res
     torch.cuda.empty_cache()
+
+
+def test_two_threads_at_once():
+    """Each on a stream of its own; launches do not hold the interpreter."""
+    cases = [inputs(1, 2000, 2, 40, "fp32", "scalar", seed=s) for s in (1, 2)]
+    want = [gdr.linear_backward(*c) for c in cases]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def run(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i] = gdr.linear_backward(*cases[i], stream=s)
+        s.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w[k], g[k]) for k in w)
