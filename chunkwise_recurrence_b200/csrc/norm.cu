@@ -482,7 +482,9 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kBwdBlock
     }
     float var = total(s), m2 = total(t);
     group_sum<G, true>(var, m2, sm[1]);
-    const float rstd = 1.f / sqrtf(var * inv + eps);
+    // (behind the last token a group computes on zeros, and without eps their
+    // rstd would put a NaN into its sums)
+    const float rstd = tok < ntok ? 1.f / sqrtf(var * inv + eps) : 0.f;
     m2 *= inv * rstd;
     Row o;
 #pragma unroll

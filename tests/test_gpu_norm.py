@@ -413,3 +413,26 @@ def test_more_values_than_32_bits_can_count(d):
                    dbias=res["dbias"]))
     del x, res
     torch.cuda.empty_cache()
+
+
+# eps = 0, token counts that do not fill a block's last round: sums written
+# per cluster, per group and per block, and heads that share a block
+NO_EPS = [(1, 1, 8), (1, 1, 64), (5, 1, 77), (37, 1, 128), (1, 1, 2048),
+          (7, 1, 2048), (333, 1, 1001), (701, 1, 2048), (2501, 1, 77),
+          (1501, 5, 101), (41, 3, 40)]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", NO_EPS)
+def test_gradients_without_eps(shape, dtype):
+    """(No row of these inputs is constant, so every one has an answer.)"""
+    x, w, b, dy = inputs(*shape, dtype, seed=7)
+    check_fwd(x, w, b, gdr.layer_norm(x, w, b, eps=0.0), eps=0.0)
+    check_bwd(x, w, dy, gdr.layer_norm_backward(x, w, dy, eps=0.0), eps=0.0)
+    n, H, d = shape
+    wide = torch.full((n, H * d + 24), 5.0, dtype=x.dtype, device="cuda")
+    wide[:, 8:8 + H * d] = x.view(n, H * d)
+    xs = wide[:, 8:8 + H * d].unflatten(-1, (H, d))
+    if xs.data_ptr() % 16 == 0:
+        check_bwd(x, w, dy, gdr.layer_norm_backward(xs, w, dy, eps=0.0),
+                  eps=0.0)
