@@ -38,6 +38,7 @@
 #include <cstdint>
 
 #include "gdr_internal.h"
+#include "norm_rows.h"
 #include "sm100.cuh"
 #include "streaming.cuh"
 
@@ -236,8 +237,8 @@ struct Rows {
     slots = reinterpret_cast<raw_t *>(sm) + threadIdx.x;
     ntok = ntok_;
     const int l = threadIdx.x % G;
-    shift = A == kShifted ? (int)(at & (V - 1)) : 0;
-    const int nv = q.active ? (shift + d + V - 1) / V : 0;
+    shift = A == kShifted ? rows::shift(at, V) : 0;
+    const int nv = q.active ? rows::vectors(shift, d, V) : 0;
     n = nv <= l ? 0 : min((nv - l + G - 1) / G, NV);
     if constexpr (A == kShifted) {
       valid = 0;
@@ -274,10 +275,9 @@ struct Rows {
         for (int j = 0; j < NV; ++j) {
           const T *p = vec(i, tok, j);
           int bytes = tok < ntok && mine(j) ? (int)sizeof(raw_t) : 0;
-          if (A == kShifted && bytes && tok == ntok - 1)
-            // (the tensor may end within its last row's last vector)
-            bytes = (int)min((long long)bytes,
-                             (long long)(end[i] - p) * (int)sizeof(T));
+          if (A == kShifted && bytes)
+            bytes = rows::vector_bytes(tok, ntok, end[i] - p, V,
+                                       (int)sizeof(T));
           copy_async<sizeof(raw_t)>(slots + stage * kStage + (i * NV + j) * B,
                                     p, bytes);
         }

@@ -436,3 +436,14 @@ def test_gradients_without_eps(shape, dtype):
     if xs.data_ptr() % 16 == 0:
         check_bwd(x, w, dy, gdr.layer_norm_backward(xs, w, dy, eps=0.0),
                   eps=0.0)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(10, 1, 1), (9, 1, 3), (5, 2, 2),
+                                   (13, 3, 1), (700, 1, 5), (41, 2, 3)])
+def test_tokens_narrower_than_a_vector(shape, dtype):
+    """Several tokens to a 16-byte vector; the last ones' vectors end with the
+    tensor."""
+    x, w, b, dy = inputs(*shape, dtype, seed=8)
+    check_fwd(x, w, b, gdr.layer_norm(x, w, b))
+    check_bwd(x, w, dy, gdr.layer_norm_backward(x, w, dy))

@@ -2,6 +2,7 @@
 references are pinned by closed forms and central differences, and the C ABI
 rejects bad arguments on the host before any CUDA call."""
 import ctypes
+import subprocess
 
 import numpy as np
 import pytest
@@ -264,3 +265,51 @@ def test_norm_backward_rejects_bad_buffers(lib, monkeypatch):
     # (few tokens need no scratch)
     monkeypatch.setenv("GDR_FAULT_INJECT_ALLOC", "1")
     assert c(n=1 << 20) == OOM
+
+
+# ------------------------------------------------------- reads of norm rows
+
+_ROWS = r"""
+#include <cstdio>
+#include "norm_rows.h"
+// every row of [ntok][H][d] by 16-byte vectors: nothing outside the tensor is
+// read, and every element of the row is
+int main() {
+  using namespace gdr::rows;
+  for (int es = 2; es <= 4; es += 2)
+    for (int ntok = 1; ntok <= 20; ++ntok)
+      for (int H = 1; H <= 4; ++H)
+        for (int d = 1; d <= 20; ++d) {
+          const int V = 16 / es;
+          const long long all = (long long)ntok * H * d;
+          for (int tok = 0; tok < ntok; ++tok)
+            for (int h = 0; h < H; ++h) {
+              const long long at = ((long long)tok * H + h) * d;
+              const int s = shift(at, V), n = vectors(s, d, V);
+              long long covered = at - s;
+              for (int i = 0; i < n; ++i) {
+                const long long from = at - s + i * V;
+                const int b = vector_bytes(tok, ntok, all - from, V, es);
+                if (from < 0 || from % V || b <= 0 ||
+                    from * es + b > all * es) {
+                  std::printf("es %d ntok %d H %d d %d tok %d h %d: %lld + %d "
+                              "of %lld bytes", es, ntok, H, d, tok, h,
+                              from * es, b, all * es);
+                  return 1;
+                }
+                covered = from + b / es;
+              }
+              if (covered < at + d) return 2;
+            }
+        }
+}
+"""
+
+
+def test_norm_rows_are_read_within_their_tensor(tmp_path):
+    src, exe = tmp_path / "rows.cpp", tmp_path / "rows"
+    src.write_text(_ROWS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", gdr_build.CSRC,
+                    str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
