@@ -267,20 +267,27 @@ struct Rows {
   __device__ __forceinline__ const T *vec(int i, long long tok, int j) const {
     return src[i] + tok * ld[i] + j * G * V;
   }
+  // END: the tensor may end within one of the token's vectors
+  template <bool END>
+  __device__ __forceinline__ void send_all(int stage, long long tok) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const T *p = vec(i, tok, j);
+        int bytes = tok < ntok && mine(j) ? (int)sizeof(raw_t) : 0;
+        if (END && bytes)
+          bytes = rows::vector_bytes(end[i] - p, V, (int)sizeof(T));
+        copy_async<sizeof(raw_t)>(slots + stage * kStage + (i * NV + j) * B, p,
+                                  bytes);
+      }
+  }
   __device__ __forceinline__ void send(int stage, long long tok) {
     if constexpr (kAsync) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const T *p = vec(i, tok, j);
-          int bytes = tok < ntok && mine(j) ? (int)sizeof(raw_t) : 0;
-          if (A == kShifted && bytes)
-            bytes = rows::vector_bytes(tok, ntok, end[i] - p, V,
-                                       (int)sizeof(T));
-          copy_async<sizeof(raw_t)>(slots + stage * kStage + (i * NV + j) * B,
-                                    p, bytes);
-        }
+      if (A == kShifted && rows::may_end(tok, ntok, V))
+        send_all<true>(stage, tok);
+      else
+        send_all<false>(stage, tok);
       copies_sent();
     }
   }

@@ -19,13 +19,16 @@ GDR_ROWS_FN int vectors(int shift, int d, int V) {
   return (shift + d + V - 1) / V;
 }
 
-// Bytes to read of a vector of a row of token `tok`, with `left` elements of
-// `es` bytes from its start to the tensor's end.  A row's last vector holds up
-// to V - 1 elements of what follows, and every later token has at least one:
-// the tensor can end within it in the last V - 1 tokens.
-GDR_ROWS_FN int vector_bytes(long long tok, int ntok, long long left, int V,
-                             int es) {
-  return tok > ntok - V && left < V ? (int)left * es : V * es;
+// Whether the tensor can end within a vector of a row of token `tok`: its last
+// one holds up to V - 1 elements of what follows, and every later token has at
+// least one.
+GDR_ROWS_FN bool may_end(long long tok, int ntok, int V) {
+  return tok > ntok - V;
+}
+// Bytes to read then, with `left` elements of `es` bytes from the vector's
+// start to the tensor's end.
+GDR_ROWS_FN int vector_bytes(long long left, int V, int es) {
+  return left < V ? (int)left * es : V * es;
 }
 
 }  // namespace rows

@@ -289,7 +289,8 @@ int main() {
               long long covered = at - s;
               for (int i = 0; i < n; ++i) {
                 const long long from = at - s + i * V;
-                const int b = vector_bytes(tok, ntok, all - from, V, es);
+                const int b = may_end(tok, ntok, V)
+                                  ? vector_bytes(all - from, V, es) : 16;
                 if (from < 0 || from % V || b <= 0 ||
                     from * es + b > all * es) {
                   std::printf("es %d ntok %d H %d d %d tok %d h %d: %lld + %d "
