@@ -548,7 +548,7 @@ struct Slots {
     if constexpr (GATE == GDR_GATE_SCALAR) {
 #pragma unroll
       for (int r = 0; r < kR; ++r)
-        sc[r] = t + r < end && has ? __ldg(la + (long long)r * ldg) : 0.f;
+        sc[r] = t + r < end && has ? load(la + (long long)r * ldg) : 0.f;
     }
     if constexpr (kTwo) {
       x += (long long)span * ldx;
@@ -684,13 +684,13 @@ struct Rows {
     float v[ROWS];
     if (have == ROWS && n == kRow) {
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) v[r] = __ldg(src + (long long)r * ld);
+      for (int r = 0; r < ROWS; ++r) v[r] = load(src + (long long)r * ld);
     } else {
       if (lane() >= n) have = 0;
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
         v[r] = 0.f;
-        if (r < have) v[r] = __ldg(src + (long long)r * ld);
+        if (r < have) v[r] = load(src + (long long)r * ld);
       }
     }
 #pragma unroll
@@ -709,8 +709,8 @@ struct Rows {
     };
     auto read = [&](const char *p, int bytes) {
       uint32_t v = 0;
-      if (bytes >= 4) v = __ldg(reinterpret_cast<const uint32_t *>(p));
-      if (bytes == 2) v = __ldg(reinterpret_cast<const unsigned short *>(p));
+      if (bytes >= 4) v = load(reinterpret_cast<const uint32_t *>(p));
+      if (bytes == 2) v = load(reinterpret_cast<const unsigned short *>(p));
       return v;
     };
     const int r0 = lane() / 16, j = lane() % 16;
@@ -722,7 +722,7 @@ struct Rows {
     if (have == ROWS && n == kRow) {       // (then words 0 .. 15 are whole)
 #pragma unroll
       for (int r = 0; r < ROWS; r += 2)
-        v[r / 2] = __ldg(
+        v[r / 2] = load(
             reinterpret_cast<const uint32_t *>(p + (long long)r * (2 * ld)));
     } else {
 #pragma unroll
@@ -784,7 +784,7 @@ struct Rows {
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         const int row = sub() * kR + r;
-        m[r][0] = row < have ? __ldg(la + (at0 + row) * ldg) : 0.f;
+        m[r][0] = row < have ? load(la + (at0 + row) * ldg) : 0.f;
       }
     }
     __syncwarp();
@@ -1354,12 +1354,12 @@ __global__ void __launch_bounds__(128)
   const int ch = (int)(i - n * nv) * V;
   float xf[kV], h[kV] = {0.f, 0.f, 0.f, 0.f};
   if constexpr (VEC)
-    unpack(__ldg(reinterpret_cast<const typename Raw<T>::type *>(
+    unpack(load(reinterpret_cast<const typename Raw<T>::type *>(
                x + n * ldx + ch)),
            xf);
   else
     xf[0] = to_float(x[n * ldx + ch]);
-  if (sin) {   // (may be sout: not through the read-only path)
+  if (sin) {   // (may be sout)
     const float *sp = sin + n * D + ch;
     if constexpr (VEC)
       unpack(*reinterpret_cast<const float4 *>(sp), h);
@@ -1370,11 +1370,11 @@ __global__ void __launch_bounds__(128)
     float g[kV];
     if constexpr (GATE == GDR_GATE_CHANNEL) {
       if constexpr (VEC)
-        unpack(__ldg(reinterpret_cast<const float4 *>(la + n * D + ch)), g);
+        unpack(load(reinterpret_cast<const float4 *>(la + n * D + ch)), g);
       else
-        g[0] = __ldg(la + n * D + ch);
+        g[0] = load(la + n * D + ch);
     } else {
-      g[0] = __ldg(la + n * H + ch / d);
+      g[0] = load(la + n * H + ch / d);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)

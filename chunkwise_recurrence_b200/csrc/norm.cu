@@ -303,7 +303,7 @@ struct Rows {
         if constexpr (kAsync)
           v = slots[stage * kStage + (i * NV + j) * B];
         else if (tok < ntok && mine(j))
-          v = __ldg(reinterpret_cast<const raw_t *>(vec(i, tok, j)));
+          v = load(reinterpret_cast<const raw_t *>(vec(i, tok, j)));
         unpack(v, f + j * V);
       }
       r[i].set(f);
@@ -351,12 +351,12 @@ struct Rows {
 #pragma unroll
         for (int e = 0; e < kE; e += 4)
           if (has(e))
-            unpack(__ldg(reinterpret_cast<const float4 *>(p + column(e))),
+            unpack(load(reinterpret_cast<const float4 *>(p + column(e))),
                    f + e);
       } else {
 #pragma unroll
         for (int e = 0; e < kE; ++e)
-          if (has(e)) f[e] = __ldg(p + column(e));
+          if (has(e)) f[e] = load(p + column(e));
       }
     }
     r.set(f);

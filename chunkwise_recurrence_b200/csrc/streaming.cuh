@@ -24,6 +24,13 @@ __device__ __forceinline__ void prior_done() {
 __device__ __forceinline__ void next_may_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// Reads what the launch before may have written, after prior_done().  An
+// ordinary load: the read-only path (__ldg) is for what nothing writes from
+// this kernel's first block on, and the wait does not order it.
+template <typename T>
+__device__ __forceinline__ T load(const T *p) {
+  return *p;
+}
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem,
                    int cluster, bool early, cudaStream_t stream, A... args) {

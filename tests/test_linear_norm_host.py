@@ -2,6 +2,7 @@
 references are pinned by closed forms and central differences, and the C ABI
 rejects bad arguments on the host before any CUDA call."""
 import ctypes
+import os
 import subprocess
 
 import numpy as np
@@ -314,3 +315,20 @@ def test_norm_rows_are_read_within_their_tensor(tmp_path):
                     str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+# --------------------------------------------- loads of overlapping launches
+
+def test_kernels_that_start_early_do_not_use_the_read_only_path():
+    """A kernel that may start while the one before it still writes must read
+    what that one wrote by ordinary loads: the wait for it does not order
+    those of the read-only path."""
+    early = []
+    for path in gdr_build.sources():
+        with open(path) as f:
+            text = f.read()
+        if "prior_done" in text:
+            early.append(os.path.basename(path))
+            assert "__ldg" not in text and "ld.global.nc" not in text, path
+            assert "__restrict__" not in text, path
+    assert early == ["linear.cu", "norm.cu"]
