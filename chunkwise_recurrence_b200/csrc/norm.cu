@@ -192,6 +192,15 @@ __device__ __forceinline__ float total(Pair p) {
   return a + b;
 }
 
+// sum / d, rounded once (inv = 1 / d): a row of one value over and over, whose
+// sum is exact, has exactly that mean.  sum * inv alone is a step off for one
+// in eight of such rows, and 1 / sqrt(eps) makes 0.3 of it where the value is
+// 16000 (1000 channels).
+__device__ __forceinline__ float mean_of(float sum, float inv, float d) {
+  const float m = sum * inv;
+  return fmaf(fmaf(-d, m, sum), inv, m);
+}
+
 // How rows are read and written.
 enum Access {
   kAligned,   // 16-byte vectors, rows start on 16-byte boundaries
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kFwdBlock
   RW rows;
   rows.start(slots, q, d, ntok, (tb + q.kk) * ldx + pc);
   rows.tensor(0, x + pc, ldx, x + ntok * ldo);
-  const float inv = 1.f / (float)d;
+  const float df = (float)d, inv = 1.f / df;
   Row wr, br;
 #pragma unroll
   for (int i = 0; i < RW::kAhead; ++i) rows.send(i, tb + q.kk + i * stride);
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kFwdBlock
     for (int i = 0; i < kE / 2; ++i) s = add2(s, r[0].p[i]);
     float mean = total(s), none = 0.f;
     group_sum<G, false>(mean, none, sm[0]);
-    mean *= inv;
+    mean = mean_of(mean, inv, df);
     Row c;
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i) c.p[i] = add2(r[0].p[i], both(-mean));
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kBwdBlock
   rows.start(slots, q, d, ntok, (tb + q.kk) * ldx + pc);
   rows.tensor(0, x + pc, ldx, x + ntok * ldo);
   rows.tensor(1, dy + pc, ldo, dy + ntok * ldo);
-  const float inv = 1.f / (float)d;
+  const float df = (float)d, inv = 1.f / df;
 #pragma unroll
   for (int i = 0; i < RW::kAhead; ++i) rows.send(i, tb + q.kk + i * stride);
   Row wr, aw, ab;
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(block_of(G), block_of(G) > 256 ? 1 : kBwdBlock
     }
     float mean = total(s), m1 = total(t);
     group_sum<G, true>(mean, m1, sm[0]);
-    mean *= inv;
+    mean = mean_of(mean, inv, df);
     m1 *= inv;
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i)

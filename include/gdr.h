@@ -705,9 +705,10 @@ GDR_API gdr_status gdr_linear_backward(
  * zeros); out [ntok][H][d] in `dtype` (written; must not overlap the rest).
  * 1 <= d <= 16384, H <= 65535, ntok H < 2^31, eps >= 0.  ntok H == 0 is a
  * no-op.  Statistics in fp32, the variance from distances to the mean; y is
- * rounded once.  A row with an infinity or NaN gives NaN; a constant row with
- * eps = 0 too (0 / 0).  One launch, no scratch.  Status codes as for
- * gdr_linear_fwd.
+ * rounded once.  A row with an infinity or NaN gives NaN.  A constant row
+ * gives the bias if its sum is exact in fp32 (every bf16 value); with eps = 0
+ * it has no answer (0 / 0, or what the mean's rounding leaves).  One launch,
+ * no scratch.  Status codes as for gdr_linear_fwd.
  */
 GDR_API gdr_status gdr_layer_norm(const void *x, long long ldx,
                                   const float *weight, const float *bias,

@@ -447,3 +447,20 @@ def test_tokens_narrower_than_a_vector(shape, dtype):
     x, w, b, dy = inputs(*shape, dtype, seed=8)
     check_fwd(x, w, b, gdr.layer_norm(x, w, b))
     check_bwd(x, w, dy, gdr.layer_norm_backward(x, w, dy))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("d", [3, 37, 77, 640, 1000, 1001, 2047, 2048, 3030,
+                               5120, 12000, 16384])
+def test_constant_rows_have_no_distances(d, dtype):
+    """Values of 8 bits, so that a row's sum is exact: of every size the
+    rows' answer is the bias, and the weight gets no gradient."""
+    v = torch.arange(128, 256, dtype=torch.float32)
+    v = torch.cat([v, -v / 128, v * 256, v / 2 ** 20]).to(DT[dtype]).cuda()
+    x = v[:, None].expand(-1, d).contiguous()
+    w, b = torch.randn(d, device="cuda"), torch.randn(d, device="cuda")
+    y = gdr.layer_norm(x, w, b)
+    assert torch.equal(y, b.to(x.dtype).expand(len(v), d))
+    g = gdr.layer_norm_backward(x, w, torch.randn_like(x))
+    assert not g["dweight"].any()
+    assert torch.isfinite(g["dx"]).all()
