@@ -619,13 +619,15 @@ GDR_API gdr_status gdr_efla_beta_backward(const void *k, const float *beta,
  * non-decreasing within [0, T]; rows of out outside every sequence are left
  * as they were.  Buffers that are written must not overlap any other.
  *
- * NaN stays in its sequence and channel; an infinity in x or in a state is
- * NaN one token on (decays near 1 are applied as h + (alpha - 1) h), and so
- * may be a state after decays > 1 whose product alone is beyond fp32.
+ * NaN stays in its sequence and channel.  With a gate, an infinity in x or in
+ * a state is NaN one token on (decays near 1 are applied as h + (alpha - 1) h),
+ * and so may be a state after decays > 1 whose product alone is beyond fp32; a
+ * product of decays below 2^-126 counts as 0.
  *
- * Sizes: B, T, H >= 0, d >= 1, H <= 65535, H d <= 2^24; at most 2^28
- * (sequence, 32-channel) pairs.  State and sums are fp32; out is rounded
- * once.  ldx < 2^30.  opts->algo must be AUTO.  One launch, no scratch;
+ * Sizes: B, T, H >= 0, d >= 1, H <= 65535, H d <= 2^24; B T < 2^30 (packed:
+ * T < 2^30), ldx < 2^30; sequences times channel tiles < 2^28, a tile being
+ * 32 channels (with a SCALAR decay of one head).  State and sums are fp32; out
+ * is rounded once.  opts->algo must be AUTO.  One launch, no scratch;
  * results do not depend on scheduling.  Where a sequence is cut across blocks
  * they wait for one another's states, bounded: an expired wait is reported
  * by gdr_device_error as GDR_ERR_TIMEOUT, and the results are not to be used
@@ -703,12 +705,13 @@ GDR_API gdr_status gdr_linear_backward(
  * Device pointers, 16-byte aligned: x [ntok][H][d] in `dtype`, tokens
  * ldx >= H d elements apart; weight and bias [H][d] fp32, or NULL (ones,
  * zeros); out [ntok][H][d] in `dtype` (written; must not overlap the rest).
- * 1 <= d <= 16384, H <= 65535, ntok H < 2^31, eps >= 0.  ntok H == 0 is a
- * no-op.  Statistics in fp32, the variance from distances to the mean; y is
- * rounded once.  A row with an infinity or NaN gives NaN.  A constant row
- * gives the bias if its sum is exact in fp32 (every bf16 value); with eps = 0
- * it has no answer (0 / 0, or what the mean's rounding leaves).  One launch,
- * no scratch.  Status codes as for gdr_linear_fwd.
+ * 1 <= d <= 16384, H <= 65535, ntok < 2^30, ntok H < 2^31, eps >= 0.
+ * ntok H == 0 is a no-op.  Statistics in fp32, the variance from distances to
+ * the mean (whose squares have to stay within fp32); y is rounded once.  A row
+ * with an infinity or NaN gives NaN.  A constant row gives the bias if its sum
+ * is exact in fp32 (every bf16 value); with eps = 0 it has no answer (0 / 0,
+ * or what the mean's rounding leaves).  One launch, no scratch.  Status codes
+ * as for gdr_linear_fwd.
  */
 GDR_API gdr_status gdr_layer_norm(const void *x, long long ldx,
                                   const float *weight, const float *bias,

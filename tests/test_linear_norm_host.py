@@ -332,3 +332,42 @@ def test_kernels_that_start_early_do_not_use_the_read_only_path():
             assert "__ldg" not in text and "ld.global.nc" not in text, path
             assert "__restrict__" not in text, path
     assert early == ["linear.cu", "norm.cu"]
+
+
+# -------------------------------------------------------------- size limits
+
+def test_size_limits_are_the_documented_ones(lib):
+    """The largest size of each kind is taken (a misaligned pointer stops the
+    call there, before any CUDA call), the next is not."""
+    with open(os.path.join(gdr_build.INCLUDE, "gdr.h")) as f:
+        text = " ".join(f.read().replace("\n *", " ").split())
+    for stated in ("B T < 2^30 (packed: T < 2^30), ldx < 2^30",
+                   "H <= 65535, H d <= 2^24",
+                   "H <= 65535, ntok < 2^30, ntok H < 2^31"):
+        assert stated in text
+    top = 1 << 30
+    one = dict(B=1, H=1, d=1, ldx=1, x=A + 8)
+    for call in (_fwd, _bwd):
+        assert call(lib, **one, T=top - 1) == INVALID
+        assert call(lib, **one, T=top) == UNSUPPORTED
+        assert call(lib, **one, T=top - 1, cu=A, nseq=1) == INVALID
+        assert call(lib, **one, T=top, cu=A, nseq=1) == UNSUPPORTED
+        wide = dict(B=1, T=1, x=A + 8)
+        assert call(lib, **wide, ldx=top - 1) == INVALID
+        assert call(lib, **wide, ldx=top) == UNSUPPORTED
+        assert call(lib, **wide, H=1, d=1 << 24, ldx=1 << 24) == INVALID
+        assert call(lib, **wide, H=1, d=(1 << 24) + 1,
+                    ldx=1 << 25) == UNSUPPORTED
+        assert call(lib, **wide, H=65535, d=1, ldx=65535) == INVALID
+        assert call(lib, **wide, H=65536, d=1, ldx=65536) == UNSUPPORTED
+    small = dict(H=1, d=1, ldx=1, x=A + 8)
+    assert _step(lib, **small, N=top - 1) == INVALID
+    assert _step(lib, **small, N=top) == UNSUPPORTED
+    for call in (_norm, _norm_bwd):
+        assert call(lib, **small, n=top - 1) == INVALID
+        assert call(lib, **small, n=top) == UNSUPPORTED
+        two = dict(H=3, d=1, ldx=3, x=A + 8)
+        assert call(lib, **two, n=((1 << 31) - 1) // 3) == INVALID
+        assert call(lib, **two, n=((1 << 31) - 1) // 3 + 1) == UNSUPPORTED
+        assert call(lib, H=1, d=16384, ldx=16384, x=A + 8) == INVALID
+        assert call(lib, H=65535, d=1, ldx=65535, x=A + 8) == INVALID
