@@ -14,6 +14,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import sysconfig
 
 import torch
 
@@ -30,7 +31,10 @@ __all__ = ["chunk_fwd", "chunk_fwd_host", "chunk_fwd_noalloc",
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdr.so")
-BINDING_PATH = os.path.join(_PKG, "_binding.so")
+# (compiled against one Python and one PyTorch, which its name gives)
+BINDING_PATH = os.path.join(
+    _PKG, f"_binding.{sysconfig.get_config_var('SOABI')}-"
+          f"torch{torch.__version__}.so")
 
 GATES = {"none": 0, "scalar": 1, "channel": 2}
 ALGOS = {"auto": 0, "staged": 1, "fused_tc": 2, "recurrent": 3}
@@ -610,12 +614,14 @@ def _load_native():
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(
                 f"{BINDING_PATH} is missing: build it with "
-                "`python -m chunkwise_recurrence_b200.build` (needs g++)")
+                "`python -m chunkwise_recurrence_b200.build` (needs g++ and "
+                "the headers of this PyTorch)")
         name = __name__ + "._binding"
         loader = importlib.machinery.ExtensionFileLoader(name, BINDING_PATH)
         spec = importlib.util.spec_from_loader(name, loader)
-        _native = importlib.util.module_from_spec(spec)
-        loader.exec_module(_native)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _native = module
     return _native
 
 

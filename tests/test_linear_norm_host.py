@@ -4,6 +4,7 @@ rejects bad arguments on the host before any CUDA call."""
 import ctypes
 import os
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -371,3 +372,65 @@ def test_size_limits_are_the_documented_ones(lib):
         assert call(lib, **two, n=((1 << 31) - 1) // 3 + 1) == UNSUPPORTED
         assert call(lib, H=1, d=16384, ldx=16384, x=A + 8) == INVALID
         assert call(lib, H=65535, d=1, ldx=65535, x=A + 8) == INVALID
+
+
+# -------------------------------------------------------------------- build
+
+def _in_another_python(code):
+    root = os.path.dirname(gdr_build.PKG)
+    return subprocess.run([sys.executable, "-c", code], cwd=root,
+                          capture_output=True, text=True)
+
+
+@pytest.mark.parametrize("missing", ["torch", "headers", "g++"])
+def test_the_library_builds_without_the_binding(lib, missing):
+    """A fresh libgdr.so: build() leaves it and does without the binding."""
+    r = _in_another_python(f"""
+import importlib.util, sys
+missing = {missing!r}
+if missing == "torch":
+    sys.modules["torch"] = None
+spec = importlib.util.spec_from_file_location("b", {gdr_build.__file__!r})
+b = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(b)
+if missing == "headers":
+    exists = b.os.path.exists
+    b.os.path.exists = lambda p: not str(p).endswith("variable.h") and exists(p)
+if missing == "g++":
+    which = b.shutil.which
+    b.shutil.which = lambda n: None if n == "g++" else which(n)
+b._stale = lambda: False
+assert b.build() == b.LIB
+try:
+    b.build_binding()
+except RuntimeError as e:
+    assert "cannot be built" in str(e)
+else:
+    raise SystemExit("the binding was built")
+""")
+    assert r.returncode == 0, r.stderr
+    assert "without its PyTorch binding" in r.stderr
+
+
+def test_the_binding_belongs_to_one_torch_and_one_python(lib, monkeypatch):
+    import sysconfig
+
+    import torch
+    assert gdr.BINDING_PATH == gdr_build.binding_path()
+    assert os.path.exists(gdr.BINDING_PATH)
+    assert not gdr_build._binding_stale()
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert gdr_build.binding_path() != gdr.BINDING_PATH
+    assert gdr_build._binding_stale()
+    monkeypatch.undo()
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "cpython-0")
+    assert gdr_build.binding_path() != gdr.BINDING_PATH
+    assert gdr_build._binding_stale()
+
+
+def test_a_missing_binding_is_an_error(lib, monkeypatch):
+    import torch
+    monkeypatch.setattr(gdr, "_native", None)
+    monkeypatch.setattr(gdr, "BINDING_PATH", gdr.BINDING_PATH + ".none")
+    with pytest.raises(RuntimeError, match="is missing"):
+        gdr.layer_norm(torch.zeros(2, 8))
