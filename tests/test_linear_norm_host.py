@@ -5,6 +5,7 @@ import ctypes
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -434,3 +435,37 @@ def test_a_missing_binding_is_an_error(lib, monkeypatch):
     monkeypatch.setattr(gdr, "BINDING_PATH", gdr.BINDING_PATH + ".none")
     with pytest.raises(RuntimeError, match="is missing"):
         gdr.layer_norm(torch.zeros(2, 8))
+
+
+def test_sources_are_compiled_side_by_side(monkeypatch, tmp_path):
+    """Nothing is compiled: the compiler is replaced by one that waits until
+    two of it run at once, and notes what it was asked to do."""
+    meet = threading.Barrier(2)
+    asked, met = [], []
+
+    def run(cmd, check):
+        assert check
+        asked.append(cmd)
+        if "-c" in cmd:
+            try:
+                meet.wait(timeout=10)
+                met.append(cmd)
+            except threading.BrokenBarrierError:
+                pass
+        else:
+            open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(gdr_build.subprocess, "run", run)
+    monkeypatch.setattr(gdr_build.os, "cpu_count", lambda: 2)
+    monkeypatch.setattr(gdr_build, "ROOT", str(tmp_path))
+    monkeypatch.setattr(gdr_build, "LIB", str(tmp_path / "libgdr.so"))
+    monkeypatch.setattr(gdr_build, "_nvcc", lambda: "nvcc")
+    monkeypatch.setattr(gdr_build, "_build_binding_if_possible",
+                        lambda force: None)
+    assert gdr_build.build(force=True) == str(tmp_path / "libgdr.so")
+    assert met
+    compiled = [c[c.index("-c") + 1] for c in asked if "-c" in c]
+    assert sorted(compiled) == gdr_build.sources()
+    objects = [a for a in asked[-1] if a.endswith(".o")]
+    assert [os.path.basename(o)[:-2] for o in objects] == \
+        [os.path.basename(s) for s in gdr_build.sources()]
