@@ -646,7 +646,9 @@ def linear_fwd(x, log_alpha=None, initial_state=None, *,
     the number of packed sequences.  Returns (out, final_state), or (out,
     final_state, chunk_states) with ``output_chunk_states``: pass the latter
     to ``linear_backward``.  final_state is None if not requested.  Rows
-    outside every packed sequence are not written.
+    outside every packed sequence are not written.  Packed sequences are best
+    of like lengths: a call is cut by their mean.  With a gate, an infinity in
+    x or in a state may turn into NaN from the next token on.
     """
     if stream is not None:
         with _on(x, stream):

@@ -29,19 +29,25 @@
 // that only their thread reads), 19 (forward) and 35 (backward) instructions
 // a value through packed fp32 pairs, four CTAs of four warps an SM so that
 // one's joins hide behind the others' arithmetic, and no cluster-wide barrier.
-// Measured (us, share of the 6.53 TB/s a copy reaches; batch x tokens x
-// channels, decay per channel, bf16 unless said):
+// Measured in short runs (us, share of the 6.53 TB/s a copy reaches; batch x
+// tokens x channels, decay per channel, bf16 unless said):
 //   forward  8 x 4096 x 2048  85 (0.97); fp32 4 x 4096 x 2048 73 (0.84);
 //            64 x 512 x 2048 84 (0.98); 1 x 65536 x 2048 201 (0.82)
 //   backward 8 x 4096 x 2048 163 (0.91); fp32 4 x 4096 x 2048 121 (0.87);
 //            1 x 65536 x 2048 350 (0.85)
+//   no decay, 8 x 4096 x 2048: forward 51 (0.80), backward 58 (0.70); fp32
+//            4 x 4096 x 2048: backward 47 (0.87)
 // One long sequence is 64 chains cut over 8 CTAs each; every step of 1024
 // tokens then waits for the slowest of the eight and for the exchange, about
 // 0.5 us of 3.1.  Longer runs of the forward pass draw the full 1000 W and
-// the clock falls to 1.78 GHz (8 x 4096 x 2048: 96 us).  A decay per head
-// leaves half the bytes and most of the arithmetic: 65 us of 42 forward, 114
-// of 68 backward.  Rows that are not aligned (H d odd) take twice the
-// instructions: 8 x 2000 x 3030 130 us (0.46).
+// the clock falls to 1.78 GHz (8 x 4096 x 2048: 91 to 100 us from one GPU to
+// another).  A decay per head leaves half the bytes and most of the
+// arithmetic: 65 us of 42 forward, 110 of 67 backward (fp32 4 x 4096 x 2048:
+// 49 of 41 and 82 of 64).  Decays below e^-1 anywhere in a warp's tile take it
+// through the dearer form of decay_factor: 8 x 4096 x 2048 with log_alpha = -2
+// 122 forward and 184 backward, -0.01 and -8 at random 135 and 203.  Rows that
+// are not aligned (H d odd) take twice the instructions: 8 x 2000 x 3030 136
+// to 139 us (0.44).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -152,7 +158,7 @@ __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[kV],
 
 // ------------------------------------------------------------------ decays
 
-// e^x, results below 2^-126 as 0
+// e^x, results below 2^-126 as 0; off by 2 + 1.2 |x| steps of 2^-23 at most
 __device__ __forceinline__ float exp_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
@@ -185,8 +191,8 @@ __device__ __forceinline__ Pair expm1_tight(Pair s) {
 
 // The decay e^s in one of two forms.  Tight (kTight <= s <= 0, the usual
 // decays): e^s - 1.  Any: for -1/8 < s <= 0 (sign bit set, also at s = 0)
-// e^s - 1, else (sign bit clear) e^s, right to its own precision however
-// small; dearer to make and to apply.
+// e^s - 1, else (sign bit clear) e^s, which keeps its digits however small it
+// is; dearer to make and to apply.
 template <bool TIGHT>
 __device__ __forceinline__ float decay_factor(float s) {
   if constexpr (TIGHT) return expm1_tight(s);
@@ -1271,7 +1277,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         renew(dr[r]);
         unpack(dr[r], g);
         add_all(cy, g);
-        const int n = t + r < end ? q.nch : 0;
+        [[maybe_unused]] const int n = t + r < end ? q.nch : 0;
         if constexpr (VEC)
           store<true>(xo + (long long)r * p.D, cy, n);
         else
@@ -1411,6 +1417,10 @@ gdr_status plan(Op op, const gdr_opts &o, LinParams *p, Plan *pl) {
   // chains
   const int wide = bwd && bf16 && pl->vec ? 16 : 8;
   const int btok = kWarps * kR * 32 / wide;
+  // Packed sequences' lengths are on the GPU, so a call is cut by their mean.
+  // One long sequence among many short ones is then cut like the short ones:
+  // 16384 tokens of 2048 channels, bf16, alone take 55 us forward and 147 in a
+  // training step, with 1000 sequences of ten tokens 704 us and 2.4 ms.
   const int avg = p->ntok / p->nseq;
   auto cut = [&](int lanes) {
     pl->lanes = lanes;
@@ -1439,7 +1449,10 @@ gdr_status plan(Op op, const gdr_opts &o, LinParams *p, Plan *pl) {
   // stays about this big, in CTAs per SM (of which four fit, six without a
   // decay): forward, bf16, 512 chains of 4096 tokens: 1 CTA 85 us, 8 CTAs 113;
   // 64 chains of 65536: 1 CTA 557 us, 8 CTAs 201; backward, a decay per
-  // channel, bf16, 256 chains of 4096: 1 CTA 170, 8 164; a decay per head, 512
+  // channel, bf16, 1, 2, 4 and 8 CTAs: 256 chains of 4096 167, 208, 175, 163;
+  // 288 178, 225, 203, 184; 384 266, 288, 249, 244; 512 403, 349, 324, 321; of
+  // 1024 tokens 256 46, 49, 46, 52; 384 71, 68, 66, 74; 512 103, 88, 85, 97 (so
+  // this rule is within a seventh of the best of each); a decay per head, 512
   // chains of 2048: 1 CTA 92, 2 101, 8 119.  fp32 gains from more as long as
   // each still has eight steps (forward, a decay per channel, 512 chains of
   // 4096: 1 CTA 148, 4 131; of 1024: 1 CTA 38, 4 41).  Where the decays are

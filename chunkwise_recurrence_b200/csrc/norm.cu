@@ -21,14 +21,18 @@
 // registers; each block (or each group, where there are few) writes one partial
 // row of them and a second kernel adds those, always in the same order.
 //
-// Measured (bf16, us, and the share of the 6.53 TB/s a copy reaches):
-// forward 32768 x 2048 45 (0.91), 8192 x 16 heads of 128 13.8 (0.74);
-// backward 32768 x 2048 69 (0.89), 8192 x 16 x 128 22 (0.70), 16384 x 4096 87
-// (0.71).  What is left of the backward pass: about 5 us for its ends and the
-// second kernel, and the two meetings a row, which two blocks an SM (128
-// registers a thread) do not hide in full.  Rows of more than 8192 channels
-// take 1024 threads of 64 registers, whose sums spill: 203 us for 4096 x 16384
-// (0.30).
+// Measured in short runs (us, and the share of the 6.53 TB/s a copy reaches;
+// bf16 unless said): forward 32768 x 2048 44 (0.93), 8192 x 16 heads of 128 12
+// (0.85), 16384 x 4096 44 (0.94), 8192 x 8192 57 (0.72), fp32 16384 x 2048 47
+// (0.87); backward 32768 x 2048 69 (0.89), 8192 x 16 x 128 21 (0.73), 16384 x
+// 4096 79 (0.78), 8192 x 8192 92 (0.67), fp32 16384 x 2048 74 (0.83).  In runs
+// of seconds 32768 x 16 heads of 128 take 48 us forward, 32768 x 2048 78
+// backward.  Rows that are not aligned take about three times as long: 32768 x
+// 2047 contiguous 121 and 206, with tokens apart 101 and 242.  What is left of
+// the backward pass: about 5 us for its ends and the second kernel, and the
+// two meetings a row, which two blocks an SM (128 registers a thread) do not
+// hide in full.  Rows of more than 8192 channels take 1024 threads of 64
+// registers, whose sums spill: 201 us for 4096 x 16384 (0.31).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

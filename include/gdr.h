@@ -620,9 +620,9 @@ GDR_API gdr_status gdr_efla_beta_backward(const void *k, const float *beta,
  * as they were.  Buffers that are written must not overlap any other.
  *
  * NaN stays in its sequence and channel.  With a gate, an infinity in x or in
- * a state is NaN one token on (decays near 1 are applied as h + (alpha - 1) h),
- * and so may be a state after decays > 1 whose product alone is beyond fp32; a
- * product of decays below 2^-126 counts as 0.
+ * a state may turn into NaN from the next token on (decays near 1 are applied
+ * as h + (alpha - 1) h), and so may a state after decays > 1 whose product
+ * alone is beyond fp32; a product of decays below 2^-126 counts as 0.
  *
  * Sizes: B, T, H >= 0, d >= 1, H <= 65535, H d <= 2^24; B T < 2^30 (packed:
  * T < 2^30), ldx < 2^30; sequences times channel tiles < 2^28, a tile being
@@ -633,7 +633,9 @@ GDR_API gdr_status gdr_efla_beta_backward(const void *k, const float *beta,
  * by gdr_device_error as GDR_ERR_TIMEOUT, and the results are not to be used
  * (the environment variable GDR_FAULT_INJECT_LINEAR_TIMEOUT=1 makes every such
  * wait expire, for tests of that path).  Fastest where H d and ldx are
- * multiples of 4 (with a SCALAR decay d as well).
+ * multiples of 4 (with a SCALAR decay d as well) and packed sequences are of
+ * like lengths: a call is cut by their mean, and one sequence of 16384 tokens
+ * among a thousand of ten takes 13 times as long as alone.
  *
  * Returns GDR_ERR_INVALID_ARGUMENT for null or misaligned pointers,
  * overlapping buffers and inconsistent sizes, GDR_ERR_UNSUPPORTED for sizes
