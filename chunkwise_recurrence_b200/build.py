@@ -79,7 +79,13 @@ def binding_needs() -> str | None:
              os.path.join(sysconfig.get_paths()["include"], "Python.h"))):
         if not os.path.exists(path):
             return what
-    return None if shutil.which("g++") else "g++"
+    if not shutil.which("g++"):
+        return "g++"
+    try:
+        _nvcc()                  # (CUDA's headers stand beside it)
+    except RuntimeError:
+        return "nvcc"
+    return None
 
 
 def _binding_stale() -> bool:

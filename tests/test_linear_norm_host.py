@@ -469,3 +469,17 @@ def test_sources_are_compiled_side_by_side(monkeypatch, tmp_path):
     objects = [a for a in asked[-1] if a.endswith(".o")]
     assert [os.path.basename(o)[:-2] for o in objects] == \
         [os.path.basename(s) for s in gdr_build.sources()]
+
+
+def test_a_fresh_library_needs_no_compiler(lib, monkeypatch, capsys):
+    """Neither for itself nor for a binding that belongs to another torch."""
+    import torch
+
+    def none():
+        raise RuntimeError("nvcc not found")
+
+    monkeypatch.setattr(gdr_build, "_stale", lambda: False)
+    monkeypatch.setattr(gdr_build, "_nvcc", none)
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert gdr_build.build() == gdr_build.LIB
+    assert "nvcc not found" in capsys.readouterr().err
